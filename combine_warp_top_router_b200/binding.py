@@ -27,6 +27,9 @@ MD_SEED_CONTIGUOUS, MD_SEED_GREEDY_PAIRS = 0, 1
 MD_REFINE_NONE, MD_REFINE_SWAPS, MD_REFINE_KL = 0, 1, 2
 MD_PERMUTE_AUTO, MD_PERMUTE_BULK, MD_PERMUTE_VECTOR = 0, 1, 2
 MD_LAYOUT_AUTO, MD_LAYOUT_COOPERATIVE, MD_LAYOUT_SPLIT = 0, 1, 2
+MD_W_NK, MD_W_KN = 0, 1
+MD_F32, MD_BF16 = 0, 1
+MD_CHECKPOINT_BLOCK = 32  # columns that share a scale of the 8-bit checkpoint
 
 _lock = threading.Lock()
 _lib = None
@@ -72,6 +75,11 @@ _SIGNATURES = {
     "md_token_shuffle_pair_workspace_size": ([_L, _I, _I], _S),
     "md_token_shuffle_pair": ([_P, _P, _I, _P, _P, _P, _L, _I, _I, ctypes.c_uint32, _P, _P, _P, _P,
                                _P, _S, _P, _P], _I),
+    "md_expert_gemm": ([_P, _L, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P], _I),
+    "md_expert_gated": ([_P, _L, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
+    "md_expert_wgrad": ([_P, _P, _L, _I, _I, _I, _P, _P, _I, _I, _P, _P, _P], _I),
+    "md_expert_gated_backward": ([_P, _P, _P, _L, _I, _P, _P, _P], _I),
+    "md_combine_backward": ([_P, _P, _L, _P, _P, _L, _I, _I, _P, _P, _P, _P], _I),
     "md_gather_rows": ([_P, _L, _L, _P, _L, _P, _P, _P], _I),
 }
 
@@ -580,6 +588,164 @@ def md_token_shuffle_pair(idx_prev, idx_l, C, C2, expert_to_rank_next, R, min_ob
                                      _stream(stream, dev))
     _check(rc, "md_token_shuffle_pair")
     return pred_rank, perm, inv, use_pair
+
+
+# ------------------------------------------------------- experts
+
+def _matrix(t, name, shape):
+    """A tensor of exactly this shape (None: any extent)."""
+    if t.dim() != len(shape) or any(want is not None and have != want
+                                    for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"{['any' if s is None else s for s in shape]}")
+    return t
+
+
+def _groups(expert_offsets, expert_counts, E, dev):
+    _need(expert_offsets, "expert_offsets", torch.int32, dev)
+    _need(expert_counts, "expert_counts", torch.int32, dev)
+    _room(expert_offsets, "expert_offsets", E)
+    _room(expert_counts, "expert_counts", E)
+
+
+def md_expert_gemm(x, w, expert_offsets, expert_counts, w_layout=MD_W_NK, out=None,
+                   dev_status=None, stream=None):
+    """y[r] = x[r] times the matrix of row r's expert (MD_W_NK: w [E, N, K], MD_W_KN: w [E, K, N]).
+
+    Rows are expert-grouped: expert_offsets and expert_counts come from md_dispatch_layout.
+    Rows of no expert are left untouched in `out`."""
+    _need(x, "x", torch.bfloat16)
+    dev = x.device
+    _need(w, "w", torch.bfloat16, dev)
+    if w_layout not in (MD_W_NK, MD_W_KN):
+        raise ValueError("w_layout must be MD_W_NK or MD_W_KN")
+    rows, K = _matrix(x, "x", (None, None)).shape
+    _matrix(w, "w", (None, None, K) if w_layout == MD_W_NK else (None, K, None))
+    E, N = w.shape[0], w.shape[1 if w_layout == MD_W_NK else 2]
+    _groups(expert_offsets, expert_counts, E, dev)
+    if out is None:
+        out = torch.empty(rows, N, dtype=torch.bfloat16, device=dev)
+    _matrix(_need(out, "out", torch.bfloat16, dev), "out", (rows, N))
+    rc = _call("md_expert_gemm", dev, _ptr(x), rows, K, _ptr(w), E, N, w_layout, _ptr(expert_offsets),
+               _ptr(expert_counts), _ptr(out), _ptr(dev_status), _stream(stream, dev))
+    _check(rc, "md_expert_gemm")
+    return out
+
+
+def md_expert_gated(x, w, expert_offsets, expert_counts, keep=False, out=None, codes=None,
+                    scales=None, dev_status=None, stream=None):
+    """Gated up-projection act = silu(g) * u with g, u = x w[e]^T; w [E, 2F, K] holds g's rows, then u's.
+
+    keep=True (or codes and scales given) also writes the 8-bit checkpoint of g and u that
+    md_expert_gated_backward reads, and returns (act, codes, scales)."""
+    _need(x, "x", torch.bfloat16)
+    dev = x.device
+    _need(w, "w", torch.bfloat16, dev)
+    rows, K = _matrix(x, "x", (None, None)).shape
+    E, N, _ = _matrix(w, "w", (None, None, K)).shape
+    if N % 2:
+        raise ValueError("w must hold as many rows for g as for u")
+    F = N // 2
+    _groups(expert_offsets, expert_counts, E, dev)
+    if out is None:
+        out = torch.empty(rows, F, dtype=torch.bfloat16, device=dev)
+    _matrix(_need(out, "out", torch.bfloat16, dev), "out", (rows, F))
+    keep = keep or codes is not None or scales is not None
+    if keep:
+        blocks = 2 * -(-F // MD_CHECKPOINT_BLOCK)
+        if codes is None:
+            codes = torch.empty(rows, N, dtype=torch.float8_e4m3fn, device=dev)
+        if scales is None:
+            scales = torch.empty(rows, blocks, dtype=torch.uint8, device=dev)
+        _matrix(_need(codes, "codes", torch.float8_e4m3fn, dev), "codes", (rows, N))
+        _matrix(_need(scales, "scales", torch.uint8, dev), "scales", (rows, blocks))
+    rc = _call("md_expert_gated", dev, _ptr(x), rows, K, _ptr(w), E, F, _ptr(expert_offsets),
+               _ptr(expert_counts), _ptr(out), _ptr(codes), _ptr(scales), _ptr(dev_status),
+               _stream(stream, dev))
+    _check(rc, "md_expert_gated")
+    return (out, codes, scales) if keep else out
+
+
+def md_expert_wgrad(dy, x, expert_offsets, expert_counts, out_dtype=torch.float32, dw=None,
+                    accumulate=False, dev_status=None, stream=None):
+    """dw[e] = sum over expert e's rows of dy[r]^T x[r], [E, N, K]; accumulate adds into a float32 dw.
+
+    E is the length of expert_counts (or dw's first extent)."""
+    _need(dy, "dy", torch.bfloat16)
+    dev = dy.device
+    _need(x, "x", torch.bfloat16, dev)
+    rows, N = _matrix(dy, "dy", (None, None)).shape
+    _, K = _matrix(x, "x", (rows, None)).shape
+    if dw is not None:
+        out_dtype = dw.dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("dw must be float32 or bfloat16")
+    if accumulate and (dw is None or out_dtype != torch.float32):
+        raise ValueError("accumulate needs a float32 dw to add to")
+    E = expert_counts.numel() if dw is None else dw.shape[0]
+    _groups(expert_offsets, expert_counts, E, dev)
+    if dw is None:
+        dw = torch.empty(E, N, K, dtype=out_dtype, device=dev)
+    _matrix(_need(dw, "dw", out_dtype, dev), "dw", (E, N, K))
+    rc = _call("md_expert_wgrad", dev, _ptr(dy), _ptr(x), rows, E, N, K, _ptr(expert_offsets),
+               _ptr(expert_counts), MD_F32 if out_dtype == torch.float32 else MD_BF16,
+               1 if accumulate else 0, _ptr(dw), _ptr(dev_status), _stream(stream, dev))
+    _check(rc, "md_expert_wgrad")
+    return dw
+
+
+def md_expert_gated_backward(da, codes, scales, dh=None, act=None, want_act=True, stream=None):
+    """(dh, act) from the gradient of the activation and the checkpoint of md_expert_gated.
+
+    dh [rows, 2F] is the gradient of g, then of u; act is the activation computed again from
+    the checkpoint (None with want_act=False)."""
+    _need(da, "da", torch.bfloat16)
+    dev = da.device
+    rows, F = _matrix(da, "da", (None, None)).shape
+    _matrix(_need(codes, "codes", torch.float8_e4m3fn, dev), "codes", (rows, 2 * F))
+    _matrix(_need(scales, "scales", torch.uint8, dev), "scales",
+            (rows, 2 * -(-F // MD_CHECKPOINT_BLOCK)))
+    if dh is None:
+        dh = torch.empty(rows, 2 * F, dtype=torch.bfloat16, device=dev)
+    if act is None and want_act:
+        act = torch.empty(rows, F, dtype=torch.bfloat16, device=dev)
+    _matrix(_need(dh, "dh", torch.bfloat16, dev), "dh", (rows, 2 * F))
+    if act is not None:
+        _matrix(_need(act, "act", torch.bfloat16, dev), "act", (rows, F))
+    rc = _call("md_expert_gated_backward", dev, _ptr(da), _ptr(codes), _ptr(scales), rows, F, _ptr(dh),
+               _ptr(act), _stream(stream, dev))
+    _check(rc, "md_expert_gated_backward")
+    return dh, act
+
+
+def md_combine_backward(dout, assign_row, topk_w, y=None, y_rows=None, dy=None, dw=None,
+                        dev_status=None, stream=None):
+    """Gradient of md_combine: (dy, dw), dy[assign_row[t, j]] = topk_w[t, j] dout[t].
+
+    dw [T, k] is the gates' gradient; it needs the expert outputs y (without y it is None).
+    dy has y's rows, or y_rows (default T * k)."""
+    _need(dout, "dout", torch.bfloat16)
+    dev = dout.device
+    _need(assign_row, "assign_row", torch.int32, dev)
+    _need(topk_w, "topk_w", torch.float32, dev)
+    T, H = _matrix(dout, "dout", (None, None)).shape
+    T, k = _matrix(topk_w, "topk_w", (T, None)).shape
+    _matrix(assign_row, "assign_row", (T, k))
+    if y is not None:
+        _matrix(_need(y, "y", torch.bfloat16, dev), "y", (None, H))
+        y_rows = y.shape[0]
+        if dw is None:
+            dw = torch.empty(T, k, dtype=torch.float32, device=dev)
+        _matrix(_need(dw, "dw", torch.float32, dev), "dw", (T, k))
+    elif dw is not None:
+        raise ValueError("dw needs y (the expert outputs)")
+    if dy is None:
+        dy = torch.empty(T * k if y_rows is None else y_rows, H, dtype=torch.bfloat16, device=dev)
+    _matrix(_need(dy, "dy", torch.bfloat16, dev), "dy", (y_rows, H))
+    rc = _call("md_combine_backward", dev, _ptr(dout), _ptr(y), dy.shape[0], _ptr(assign_row), _ptr(topk_w),
+               T, k, H, _ptr(dy), _ptr(dw), _ptr(dev_status), _stream(stream, dev))
+    _check(rc, "md_combine_backward")
+    return dy, dw
 
 
 # ------------------------------------------------------- EP exchange

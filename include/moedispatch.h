@@ -70,6 +70,11 @@ typedef enum md_status {
 #define MD_REFINE_SWAPS 1      /* best positive single swaps                */
 #define MD_REFINE_KL 2         /* Kernighan-Lin passes                      */
 
+#define MD_W_NK 0              /* expert weights [E, N, K]: output rows      */
+#define MD_W_KN 1              /* expert weights [E, K, N]: input rows       */
+#define MD_F32 0               /* element types of md_expert_wgrad's output  */
+#define MD_BF16 1
+
 #define MD_MAX_TOPK 32
 #define MD_MAX_EXPERTS 1024
 #define MD_MAX_RANKS 64
@@ -643,6 +648,106 @@ int md_pearson_from_sums(const uint64_t *sums, int64_t n, double *r);
  * defaults.  Process-wide; set them only while no other call is in flight.
  */
 void md_set_test_hooks(long long poll_limit, int layout_skip_tile, long long expand_skip_unit);
+
+/*
+ * The experts between dispatch and combine, and what their training needs.
+ * "Expert Coupling in MoE Pretraining", The Communication Bottleneck: the
+ * experts run on the dispatched rows before the combine returns them.
+ *
+ * Rows are the conventional, expert-grouped rows of md_dispatch_layout (either
+ * mode's assign_row order; md_dispatch_permute or md_dedup_expand fills them):
+ *   expert_offsets int32 [>= E]  first row of expert e
+ *   expert_counts  int32 [E]     rows of expert e; 0 is allowed
+ * Experts may stand in any order; their ranges must not overlap.  A range
+ * that leaves [0, rows) is treated as empty and reported (MD_ERR_DATA).  Rows
+ * that belong to no expert are neither read into a result nor written.
+ * Products are bf16 x bf16 on the tensor cores with float32 sums, rounded to
+ * the output type once.  NaN or Inf in one row reaches that row's results
+ * only (md_expert_wgrad: its expert's).
+ * Limits of the three products: N, K (gated: F, K) multiples of 8, N (gated:
+ * 2F) and K up to 2^20, N * K <= 2^37; E <= 1024; rows < 2^31 - 4096; all buffers 16-byte
+ * aligned.  The waits inside the kernels are bounded (MD_ERR_TIMEOUT).  One
+ * launch each, no workspace; safe in CUDA graph capture.
+ */
+
+/*
+ * md_expert_gemm -- one product per expert over its rows.
+ *   x   bf16 [rows, K]
+ *   w   bf16 [E, N, K]  MD_W_NK: y[r][n] = sum_k x[r][k] w[e][n][k]
+ *       bf16 [E, K, N]  MD_W_KN: y[r][n] = sum_k x[r][k] w[e][k][n]
+ *   y   bf16 [rows, N]  out
+ * MD_W_KN on the same weights is the input gradient of MD_W_NK (and the other
+ * way round): dx = dy w.
+ */
+int md_expert_gemm(const void *x, int64_t rows, int K, const void *w, int E, int N, int w_layout,
+                   const int32_t *expert_offsets, const int32_t *expert_counts, void *y,
+                   int32_t *dev_status, void *stream);
+
+/*
+ * md_expert_gated -- gated up-projection: product, activation and 8-bit
+ * checkpoint in one kernel.
+ *   x       bf16 [rows, K]
+ *   w       bf16 [E, 2F, K]  rows [0, F) give g, rows [F, 2F) give u
+ *   act     bf16 [rows, F]   out: g / (1 + exp(-g)) * u from the float32 g, u
+ *   codes   e4m3 [rows, 2F]  out, or NULL: the checkpoint of g, then of u
+ *   scales  uint8 [rows, 2 * ceil(F / 32)]  out, NULL with codes: for each 32
+ *           columns of g, then of u, the exponent s + 127 of their scale 2^s:
+ *           the smallest s >= -127 with max |value| <= 448 * 2^s, Inf and
+ *           NaN left out.  A code is value / 2^s rounded to e4m3 (nearest,
+ *           ties to even); Inf and NaN are stored as NaN.
+ * The checkpoint holds the pre-activations in (1 + 1/32) bytes a value
+ * instead of the 2 of bf16, each within 2^-4 of its value (relative, or
+ * 2^-10 of the scale for values below 2^-6 of it).
+ */
+int md_expert_gated(const void *x, int64_t rows, int K, const void *w, int E, int F,
+                    const int32_t *expert_offsets, const int32_t *expert_counts, void *act,
+                    void *codes, uint8_t *scales, int32_t *dev_status, void *stream);
+
+/*
+ * md_expert_wgrad -- weight gradient of md_expert_gemm with MD_W_NK:
+ *   dw[e][n][k] = sum over expert e's rows of dy[r][n] x[r][k]
+ *   dy  bf16 [rows, N], x bf16 [rows, K]
+ *   dw  [E, N, K], float32 (MD_F32) or bf16 (MD_BF16)
+ *   accumulate  1: added to dw (MD_F32 only); 0: dw is overwritten, with
+ *               zeros for experts without rows
+ * For weights in MD_W_KN order pass x and dy in each other's place.
+ */
+int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int E, int N, int K,
+                    const int32_t *expert_offsets, const int32_t *expert_counts, int out_type,
+                    int accumulate, void *dw, int32_t *dev_status, void *stream);
+
+/*
+ * md_expert_gated_backward -- the activation's gradient from the checkpoint of
+ * md_expert_gated.  With g, u the checkpoint's values and s = 1/(1+exp(-g)):
+ *   dh[r][f]     = bf16( da[r][f] u s (1 + g (1 - s)) )    (gradient of g)
+ *   dh[r][F + f] = bf16( da[r][f] g s )                    (gradient of u)
+ *   act[r][f]    = bf16( g s u )   the activation again, for the weight
+ *                  gradient of the down-projection; NULL leaves it out
+ *   da bf16 [rows, F], codes e4m3 [rows, 2F], scales uint8 [rows, 2*ceil(F/32)],
+ *   dh bf16 [rows, 2F], act bf16 [rows, F]; float32 inside.
+ * A NaN code gives NaN.  F a multiple of 8; da, codes, dh, act 16-byte
+ * aligned.
+ */
+int md_expert_gated_backward(const void *da, const void *codes, const uint8_t *scales, int64_t rows,
+                             int F, void *dh, void *act, void *stream);
+
+/*
+ * md_combine_backward -- gradient of md_combine (fused mode).
+ *   dout        bf16    [T, H]       gradient of the combined output
+ *   y           bf16    [y_rows, H]  the expert outputs md_combine read; may
+ *                                    be NULL when dw is NULL
+ *   assign_row  int32   [T, k], topk_w float32 [T, k]  as in md_combine
+ *   dy          bf16    [y_rows, H]  out: dy[assign_row[t][j]] =
+ *                                    bf16( topk_w[t][j] * dout[t] ); rows that
+ *                                    nobody names are left untouched
+ *   dw          float32 [T, k]       out, or NULL: sum_h dout[t][h] y[row][h],
+ *                                    summed in float32 in a fixed order
+ * A row index outside [0, y_rows) is skipped and reported (MD_ERR_DATA), its
+ * dw is 0.  dy must not overlap y or dout.
+ */
+int md_combine_backward(const void *dout, const void *y, int64_t y_rows, const int32_t *assign_row,
+                        const float *topk_w, int64_t T, int k, int H, void *dy, float *dw,
+                        int32_t *dev_status, void *stream);
 
 #ifdef __cplusplus
 }
