@@ -76,10 +76,11 @@ struct Bars {
 // Bounded wait of one thread; on run-out raises the CTA's abort flag.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, Bars *b, const Args &a)
 {
+    if (md::mbar_try_wait(bar, parity)) return true;
     volatile int *ab = &b->abort;
-    for (long long i = 0; i < a.polls; ++i) {
-        if (md::mbar_try_wait(bar, parity)) return true;
+    for (long long i = 1; i < a.polls; ++i) {
         if (*ab) return false;
+        if (md::mbar_try_wait(bar, parity)) return true;
     }
     *ab = 1;
     md::report(a.status, MD_ERR_TIMEOUT);
@@ -115,21 +116,35 @@ struct Tile {
     int n;           // MMA N
 };
 
+// A place in the ring of stages: the stage and the parity of its turn.
+template <int STAGES>
+struct Turn {
+    int s = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++s == STAGES) {
+            s = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
 // experts' starts, counts and the running number of tiles, in shared memory
 struct Table {
     int *off, *cnt, *pre;
 };
 
 template <int MODE, int CG, int BN>
-__device__ __forceinline__ Tile tile_at(int64_t t, const Table &tab, const Args &a, int mt, int rank)
+__device__ __forceinline__ Tile tile_at(int t, const Table &tab, const Args &a, int mt, int rank)
 {
     using P = Plan<MODE, CG, BN>;
     Tile q;
     if (P::kWg) {
         const int ct = (a.k + BN - 1) / BN;
         const int per = mt * ct;
-        q.e = (int)(t / per);
-        const int i = (int)(t - (int64_t)q.e * per);
+        q.e = t / per;
+        const int i = t - q.e * per;
         const int ci = i / mt;
         q.m0 = ((i - ci * mt) * CG + rank) * kTileM;
         q.c0 = ci * BN;
@@ -140,8 +155,8 @@ __device__ __forceinline__ Tile tile_at(int64_t t, const Table &tab, const Args 
         q.n = (w + P::kGran - 1) / P::kGran * P::kGran;
         return q;
     }
-    const int rt = (int)(t / mt);
-    const int mi = (int)(t - (int64_t)rt * mt);
+    const int rt = t / mt;
+    const int mi = t - rt * mt;
     int lo = 0, hi = a.E;  // last expert whose first tile is at or before rt
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -277,29 +292,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = b->tmem;
 
     const int mt = (a.n + P::kMWidth * CG - 1) / (P::kMWidth * CG);  // tiles along the weight rows
-    const int64_t total = P::kWg ? (int64_t)a.E * mt * ((a.k + BN - 1) / BN) : (int64_t)b->tiles * mt;
-    const int64_t first = blockIdx.x / CG, step = gridDim.x / CG;
+    const int total = P::kWg ? a.E * mt * ((a.k + BN - 1) / BN) : b->tiles * mt;  // the host keeps it below 2^31
+    const int first = blockIdx.x / CG, step = gridDim.x / CG;
     const uint32_t sbase = md::smem_addr(base);
 
     if (warp == 4) {
         // ------------------------------------------------ loads
         if (lane == 0) {
-            int64_t it = 0;
+            Turn<P::kStages> at;
+            int used = 0;  // stages loaded at least once
             bool ok = true;
-            for (int64_t t = first; ok && t < total; t += step) {
+            for (int t = first; ok && t < total; t += step) {
                 const Tile q = tile_at<MODE, CG, BN>(t, tab, a, mt, rank);
                 const int kb = P::kWg ? (q.count + kTileK - 1) / kTileK : (a.k + kTileK - 1) / kTileK;
                 const int half = q.n / CG;  // N-side lines of this CTA
                 const int boxes = P::kWg ? (half + 63) / 64 : (half + P::kBox - 1) / P::kBox;
-                const uint32_t bytes = kABytes + boxes * (P::kWg ? 8192 : P::kBox * 128);
-                for (int i = 0; i < kb; ++i, ++it) {
-                    const int s = (int)(it % P::kStages);
-                    if (!wait_for(&b->empty[s], (uint32_t)((it / P::kStages) & 1) ^ 1u, b, a)) {
+                const uint32_t bytes = (kABytes + boxes * (P::kWg ? 8192 : P::kBox * 128)) * CG;
+                const int r0 = (int)q.r0 + (P::kWg ? 0 : rank * half), c0 = q.c0 + rank * half;
+                for (int i = 0; i < kb; ++i) {
+                    const int s = at.s;
+                    if (!wait_for(&b->empty[s], at.parity ^ 1u, b, a)) {
                         ok = false;
                         break;
                     }
                     uint32_t bar = md::smem_addr(&b->full[s]);
-                    if (rank == 0) md::mbar_expect_tx(&b->full[s], bytes * CG);
+                    if (rank == 0) md::mbar_expect_tx(&b->full[s], bytes);
                     if (CG == 2) bar = md::map_rank(bar, 0);
                     const uint32_t sa = sbase + s * P::kStageBytes, sb = sa + kABytes;
                     const int k0 = i * kTileK;
@@ -312,52 +329,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                         md::tma_load_3d<CG>(sa, &map_a, q.m0, k0, q.e, bar);
                         md::tma_load_3d<CG>(sa + 8192, &map_a, q.m0 + 64, k0, q.e, bar);
                     } else {
-                        const int r = (int)(q.r0 + k0);
-                        md::tma_load_2d<CG>(sa, &map_a, q.m0, r, bar);
-                        md::tma_load_2d<CG>(sa + 8192, &map_a, q.m0 + 64, r, bar);
-                        for (int j = 0; j < boxes; ++j)
-                            md::tma_load_2d<CG>(sb + j * 8192, &map_b, q.c0 + rank * half + j * 64, r, bar);
+                        md::tma_load_2d<CG>(sa, &map_a, q.m0, r0 + k0, bar);
+                        md::tma_load_2d<CG>(sa + 8192, &map_a, q.m0 + 64, r0 + k0, bar);
                     }
-                    if (!P::kWg) {
-                        const int r = (int)q.r0 + rank * half;
-                        for (int j = 0; j < boxes; ++j)
-                            md::tma_load_2d<CG>(sb + j * P::kBox * 128, &map_b, k0, r + j * P::kBox, bar);
+                    for (int j = 0; j < boxes; ++j) {
+                        if (P::kWg) md::tma_load_2d<CG>(sb + j * 8192, &map_b, c0 + j * 64, r0 + k0, bar);
+                        else md::tma_load_2d<CG>(sb + j * P::kBox * 128, &map_b, k0, r0 + j * P::kBox, bar);
                     }
+                    if (used < P::kStages) ++used;
+                    at.next();
                 }
             }
             // await the copies in flight, whoever gave up: the last load of every stage
             if (rank == 0) {
-                for (int64_t j = it > P::kStages ? it - P::kStages : 0; j < it; ++j)
-                    md::mbar_wait_bounded(&b->full[j % P::kStages], (uint32_t)((j / P::kStages) & 1), kDrainPolls);
+                for (int j = 0; j < used; ++j) {  // backwards from the last stage loaded
+                    at.parity ^= at.s == 0 ? 1u : 0u;
+                    at.s = at.s == 0 ? P::kStages - 1 : at.s - 1;
+                    md::mbar_wait_bounded(&b->full[at.s], at.parity, kDrainPolls);
+                }
             } else if (!ok) {
                 for (int j = 0; j < 2000; ++j) __nanosleep(500);
             }
         }
     } else if (warp == 5) {
         // ------------------------------------------------ products
-        if (rank == 0) {
-            int64_t it = 0;
+        if (rank == 0 && (P::kWg || lane == 0)) {
+            constexpr bool kAKMajor = MODE == kNK || MODE == kGated;
+            const uint64_t da0 = kAKMajor ? md::operand_desc(sbase, 16, 1024) : md::operand_desc(sbase, 8192, 1024);
+            const uint64_t db0 = P::kWg ? md::operand_desc(sbase + kABytes, 8192, 1024)
+                                        : md::operand_desc(sbase + kABytes, 16, 1024);
+            constexpr int kAStep = (kAKMajor ? 32 : 2048) >> 4, kBStep = (P::kWg ? 2048 : 32) >> 4;
+            Turn<P::kStages> at;
             int acc = 0;
             bool ok = true;
-            for (int64_t t = first; ok && t < total; t += step) {
+            for (int t = first; ok && t < total; t += step) {
                 const Tile q = tile_at<MODE, CG, BN>(t, tab, a, mt, rank);
                 const int kb = P::kWg ? (q.count + kTileK - 1) / kTileK : (a.k + kTileK - 1) / kTileK;
                 if (kb == 0) continue;
                 const int buf = acc & 1;
-                const uint32_t idesc = md::mma_desc(kTileM * CG, q.n, MODE == kKN || P::kWg, P::kWg);
+                const uint32_t idesc = md::mma_desc(kTileM * CG, q.n, !kAKMajor, P::kWg);
                 const uint32_t d = tmem + buf * BN;
-                if (!warp_wait(&b->tempty[buf], (uint32_t)((acc >> 1) & 1) ^ 1u, b, a)) break;
+                const uint32_t tparity = (uint32_t)((acc >> 1) & 1) ^ 1u;
+                if (P::kWg ? !warp_wait(&b->tempty[buf], tparity, b, a) : !wait_for(&b->tempty[buf], tparity, b, a))
+                    break;
                 md::tmem_fence_after();
                 ++acc;
-                for (int i = 0; i < kb; ++i, ++it) {
-                    const int s = (int)(it % P::kStages);
-                    if (!warp_wait(&b->full[s], (uint32_t)((it / P::kStages) & 1), b, a)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sa = sbase + s * P::kStageBytes, sb = sa + kABytes;
+                for (int i = 0; i < kb; ++i) {
+                    const int s = at.s;
                     int steps = kTileK / 16;
                     if (P::kWg) {
+                        if (!warp_wait(&b->full[s], at.parity, b, a)) {
+                            ok = false;
+                            break;
+                        }
                         // the last block reaches into the next expert's rows: rows past the end
                         // are cleared on both sides (zero times a stray NaN or Inf is not zero)
                         const int v = q.count - i * kTileK;
@@ -373,34 +397,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                             md::fence_async_shared();
                             __syncwarp();
                         }
+                    } else if (!wait_for(&b->full[s], at.parity, b, a)) {
+                        ok = false;
+                        break;
                     }
                     md::tmem_fence_after();
                     if (lane == 0) {
-                        for (int j = 0; j < steps; ++j) {
-                            const uint64_t da = MODE == kNK || MODE == kGated
-                                                    ? md::operand_desc(sa + j * 32, 16, 1024)
-                                                    : md::operand_desc(sa + j * 2048, 8192, 1024);
-                            const uint64_t db = P::kWg ? md::operand_desc(sb + j * 2048, 8192, 1024)
-                                                       : md::operand_desc(sb + j * 32, 16, 1024);
-                            md::mma_bf16<CG>(d, da, db, idesc, i > 0 || j > 0);
-                        }
+                        const uint64_t da = da0 + (uint32_t)(s * (P::kStageBytes >> 4));
+                        const uint64_t db = db0 + (uint32_t)(s * (P::kStageBytes >> 4));
+#pragma unroll
+                        for (int j = 0; j < kTileK / 16; ++j)
+                            if (!P::kWg || j < steps)
+                                md::mma_bf16<CG>(d, da + j * kAStep, db + j * kBStep, idesc, i > 0 || j > 0);
                         md::mma_commit<CG>(&b->empty[s]);
                         if (i == kb - 1) md::mma_commit<CG>(&b->tfull[buf]);
                     }
-                    __syncwarp();
+                    if (P::kWg) __syncwarp();
+                    at.next();
                 }
             }
             if (lane == 0) {  // await the MMAs in flight, whoever gave up
                 md::mma_commit<CG>(&b->drain);
                 md::mbar_wait_bounded(&b->drain, 0, kDrainPolls);
             }
-            __syncwarp();
         }
     } else {
         // ------------------------------------------------ results
         int acc = 0, chunk = 0;
         const uint32_t quarter = (uint32_t)(warp * 32) << 16;
-        for (int64_t t = first; t < total; t += step) {
+        for (int t = first; t < total; t += step) {
             const Tile q = tile_at<MODE, CG, BN>(t, tab, a, mt, rank);
             const bool zero = P::kWg && q.count == 0;
             if (zero && a.accumulate) continue;
@@ -539,6 +564,7 @@ int launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md_,
            cudaStream_t s)
 {
     using P = Plan<MODE, CG, BN>;
+    if (tiles > (int64_t)1 << 30) return MD_ERR_UNSUPPORTED;
     static std::atomic<uint64_t> setup{0};
     md::once_per_device(setup, [] {
         if (cudaFuncSetAttribute(k_expert<MODE, CG, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
