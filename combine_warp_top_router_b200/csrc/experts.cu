@@ -59,8 +59,8 @@ struct Plan {
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kBox = BN >= 256 ? 64 : 16;  // x rows per TMA box
     static constexpr int kStaging = MODE == kNK || MODE == kKN ? 2 * 32 * 256 : 2 * 32 * 512;
-    static constexpr int kStages = (200 * 1024 - kStaging) / kStageBytes > 10
-                                       ? 10 : (200 * 1024 - kStaging) / kStageBytes;
+    static constexpr int kFit = (212 * 1024 - kStaging) / kStageBytes;  // leaves 12 KB for 1024 experts' table
+    static constexpr int kStages = kFit > 10 ? 10 : kFit;
     static constexpr int kCols = 2 * BN < 32 ? 32 : 2 * BN;  // TMEM columns: two accumulators
     static constexpr int kMWidth = MODE == kGated ? 64 : kTileM;  // output columns per CTA
     static size_t smem(int E) { return 1024 + (size_t)kStages * kStageBytes + kStaging + 12 * (size_t)E + 16; }
@@ -653,9 +653,9 @@ extern "C" int md_expert_gemm(const void *x, int64_t rows, int K, const void *w,
     a.polls = md::hook_poll_limit(kPolls);
     if (w_layout == MD_W_NK)
         return few_rows(rows, E) ? run_rows<kNK, 1, 64>(x, w, rows, a, K, N, s)
-                                 : run_rows<kNK, 1, 256>(x, w, rows, a, K, N, s);
+                                 : run_rows<kNK, 2, 256>(x, w, rows, a, K, N, s);
     return few_rows(rows, E) ? run_rows<kKN, 1, 64>(x, w, rows, a, N, K, s)
-                             : run_rows<kKN, 1, 256>(x, w, rows, a, N, K, s);
+                             : run_rows<kKN, 2, 256>(x, w, rows, a, N, K, s);
 }
 
 extern "C" int md_expert_gated(const void *x, int64_t rows, int K, const void *w, int E, int F,
@@ -684,7 +684,7 @@ extern "C" int md_expert_gated(const void *x, int64_t rows, int K, const void *w
     a.status = dev_status;
     a.polls = md::hook_poll_limit(kPolls);
     return few_rows(rows, E) ? run_rows<kGated, 1, 64>(x, w, rows, a, K, 2 * (int64_t)F, s)
-                             : run_rows<kGated, 1, 256>(x, w, rows, a, K, 2 * (int64_t)F, s);
+                             : run_rows<kGated, 2, 256>(x, w, rows, a, K, 2 * (int64_t)F, s);
 }
 
 extern "C" int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int E, int N, int K,
