@@ -7,20 +7,22 @@
 //   gated  a[r, f]     = silu(g) u,  g = w[e, f] . x[r],  u = w[e, F + f] . x[r]
 //   wgrad  dw[e, n, k] = sum_{r of e} dy[r, n] x[r, k]
 //
-// One persistent kernel body.  The tensor cores' M axis (128 rows per CTA) holds weight
-// rows n, their N axis holds the ragged rows r (for the weight gradient: the
-// columns k).  The N extent of an MMA is free in steps of 16, so an expert's
-// ragged remainder costs what it holds: an expert's c rows are split into
-// ceil(c / BN) equal tiles, and each tile's MMAs are issued with its own N.
-// Putting the rows on the M axis instead would pay for 128 rows per remainder,
-// which at a few rows per expert (decoding) is nearly all of the work.
+// Two persistent kernels: k_expert_few for calls with few rows to an expert, which
+// are bound by reading the weights, and k_expert_wide for many, which are bound by
+// the tensor cores and by the path from L2.  In both, the tensor cores' M axis
+// (128 rows per CTA) holds weight rows n, their N axis the ragged rows r (weight
+// gradient: the columns k).  The N extent of an MMA is free in steps of 16 (32 for
+// a pair of CTAs), so an expert's ragged remainder costs what it holds: its c rows
+// are split into ceil(c / BN) equal tiles, and each tile's MMAs are issued with
+// its own N.  Rows on the M axis would pay for 128 rows per remainder, which at a
+// few rows per expert (decoding) is nearly all of the work.
 //
-// Warps 0-3 drain accumulators (TMEM -> registers -> shared -> global), warp 4
-// issues the TMA loads, warp 5 the MMAs; accumulators are double-buffered in
-// TMEM, so a tile's epilogue runs under the next tile's products.  Every wait
-// is bounded: the role whose wait runs out raises the CTA's abort flag and
-// MD_ERR_TIMEOUT, all roles leave their loops, copies and MMAs in flight are
-// awaited (bounded again), TMEM is freed, and the kernel returns.
+// Warps 0-7 drain accumulators (TMEM -> registers -> shared -> global; two
+// groups of four, one warp for each quarter of TMEM's lanes); one warp issues
+// the MMAs and one or two the TMA loads.  Every wait is bounded: the role whose
+// wait runs out raises the CTA's abort flag and MD_ERR_TIMEOUT, all roles leave
+// their loops, copies and MMAs in flight are awaited (bounded again), TMEM is
+// freed, and the kernel returns.
 #include "tcgen05.cuh"
 
 namespace {
@@ -29,10 +31,11 @@ enum { kNK, kKN, kGated, kWgrad };
 
 constexpr int kTileM = 128;  // weight rows per CTA
 constexpr int kTileK = 64;   // 128 bytes of bf16: one swizzled line
-constexpr int kEpiWarps = 4;
-constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kEpiWarps = 8;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kLoadXWarp = 10;
 constexpr int kABytes = kTileM * kTileK * 2;
 constexpr int kBlock = 32;   // columns that share a scale of the 8-bit checkpoint
+constexpr int kMaxSplit = 4; // CTAs that share a contraction (few rows)
 constexpr long long kPolls = 1ll << 22;
 constexpr long long kDrainPolls = 1ll << 20;
 
@@ -43,41 +46,27 @@ struct Args {
     int n;        // weight rows per expert that tiles cover (gemm: N, gated: F, wgrad: N)
     int k;        // extent of the contraction (gemm, gated: K); wgrad: columns of dw
     int pitch;    // columns of y, or of a
-    void *y;      // gemm: bf16 [rows, N]; gated: bf16 [rows, F]
+    void *y;      // gemm: bf16 [rows, N]; gated: bf16 [rows, F]; wgrad: dw
     uint8_t *codes, *scales;  // gated: checkpoint or NULL
-    int out_bf16, accumulate; // wgrad
+    int out_bf16, accumulate, sectors;  // wgrad; sectors: dw is 32-byte aligned
+    int subs;     // k_expert_wide: M = 256 products to a tile, at most
+    int split;    // k_expert_few: CTAs (a cluster) that share each tile's contraction; each cluster has one tile
     int32_t *status;
     long long polls;
 };
 
-template <int MODE, int CG, int BN>
-struct Plan {
-    static constexpr bool kWg = MODE == kWgrad;
-    static constexpr int kGran = 16 * CG;             // step of an MMA's N
-    static constexpr int kBRows = BN / CG;            // N-side lines per CTA
-    static constexpr int kBBytes = kBRows * kTileK * 2;
-    static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kBox = BN >= 256 ? 64 : 16;  // x rows per TMA box
-    static constexpr int kStaging = MODE == kNK || MODE == kKN ? 2 * 32 * 256 : 2 * 32 * 512;
-    static constexpr int kFit = (212 * 1024 - kStaging) / kStageBytes;  // leaves 12 KB for 1024 experts' table
-    static constexpr int kStages = kFit > 10 ? 10 : kFit;
-    static constexpr int kCols = 2 * BN < 32 ? 32 : 2 * BN;  // TMEM columns: two accumulators
-    static constexpr int kMWidth = MODE == kGated ? 64 : kTileM;  // output columns per CTA
-    static size_t smem(int E) { return 1024 + (size_t)kStages * kStageBytes + kStaging + 12 * (size_t)E + 16; }
-};
-
-struct Bars {
-    uint64_t full[10], empty[10], tfull[2], tempty[2], drain;
+// What the roles of a CTA share, besides their barriers.
+struct Shared {
     uint32_t tmem;
     int abort;
-    int tiles;  // ragged tiles of all experts
+    int tiles;  // ragged row tiles of all experts
 };
 
 // Bounded wait of one thread; on run-out raises the CTA's abort flag.
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, Bars *b, const Args &a)
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, Shared *sh, const Args &a)
 {
     if (md::mbar_try_wait(bar, parity)) return true;
-    volatile int *ab = &b->abort;
+    volatile int *ab = &sh->abort;
     for (long long i = 1; i < a.polls; ++i) {
         if (*ab) return false;
         if (md::mbar_try_wait(bar, parity)) return true;
@@ -88,19 +77,20 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, Bars *b
 }
 
 // The same for a whole warp: lane 0 waits, all lanes get its answer.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Bars *b, const Args &a)
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Shared *sh, const Args &a)
 {
     int ok = 0;
-    if ((threadIdx.x & 31) == 0) ok = wait_for(bar, parity, b, a);
+    if ((threadIdx.x & 31) == 0) ok = wait_for(bar, parity, sh, a);
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-// Whether all of the epilogue's warps say yes (they share barriers, so they
-// leave together).
-__device__ __forceinline__ bool all_warps(bool ok)
+// Wait of the epilogue's warps: the first polls, the others sleep at a barrier,
+// and all get its answer (they share barriers, so they leave together).
+__device__ __forceinline__ bool epilogue_wait(uint64_t *bar, uint32_t parity, Shared *sh, const Args &a)
 {
+    const bool ok = threadIdx.x >= 32 || warp_wait(bar, parity, sh, a);
     int r;
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.and.pred q, 2, %2, p;\n"
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.and.pred q, 1, %2, p;\n"
                  " selp.s32 %0, 1, 0, q;\n}"
                  : "=r"(r)
                  : "r"((int)ok), "n"(kEpiWarps * 32)
@@ -110,68 +100,135 @@ __device__ __forceinline__ bool all_warps(bool ok)
 
 struct Tile {
     int e, m0;       // expert, first weight row of the CTA (pair: of its half)
-    int64_t r0;      // gemm: first x row; wgrad: first row of the expert
-    int count;       // gemm: rows of the tile; wgrad: rows of the expert
+    int64_t r0;      // first x row (wgrad: of the expert)
+    int count;       // rows (wgrad: of the expert)
     int c0;          // wgrad: first dw column
     int n;           // MMA N
 };
 
 // A place in the ring of stages: the stage and the parity of its turn.
-template <int STAGES>
 struct Turn {
+    int stages;
     int s = 0;
     uint32_t parity = 0;
+    __device__ __forceinline__ explicit Turn(int n) : stages(n) {}
     __device__ __forceinline__ void next()
     {
-        if (++s == STAGES) {
+        if (++s == stages) {
             s = 0;
+            parity ^= 1u;
+        }
+    }
+    __device__ __forceinline__ void back()
+    {
+        if (s-- == 0) {
+            s = stages - 1;
             parity ^= 1u;
         }
     }
 };
 
-// experts' starts, counts and the running number of tiles, in shared memory
+// Await the copies in flight, whoever gave up: the last load of each stage.
+__device__ __forceinline__ void drain_loads(Turn at, int used, uint64_t *full)
+{
+    for (int j = 0; j < used; ++j) {
+        at.back();
+        md::mbar_wait_bounded(&full[at.s], at.parity, kDrainPolls);
+    }
+}
+
+// Experts' starts and counts, the running number of row tiles, and the
+// experts in the order of their tiles; in shared memory.
 struct Table {
-    int *off, *cnt, *pre;
+    int *off, *cnt, *pre, *order;
+    __device__ __forceinline__ Table(void *at, int E)
+        : off(static_cast<int *>(at)), cnt(off + E), pre(cnt + E), order(pre + E) {}
+    static size_t bytes(int E) { return 16 * (size_t)E; }
 };
 
-template <int MODE, int CG, int BN>
-__device__ __forceinline__ Tile tile_at(int t, const Table &tab, const Args &a, int mt, int rank)
+// The experts' ranges, checked, by all threads.
+__device__ __forceinline__ void read_ranges(const Table &tab, const Args &a)
 {
-    using P = Plan<MODE, CG, BN>;
-    Tile q;
-    if (P::kWg) {
-        const int ct = (a.k + BN - 1) / BN;
-        const int per = mt * ct;
-        q.e = t / per;
-        const int i = t - q.e * per;
-        const int ci = i / mt;
-        q.m0 = ((i - ci * mt) * CG + rank) * kTileM;
-        q.c0 = ci * BN;
-        q.r0 = tab.off[q.e];
-        q.count = tab.cnt[q.e];
-        const int left = a.k - q.c0;
-        const int w = left < BN ? left : BN;
-        q.n = (w + P::kGran - 1) / P::kGran * P::kGran;
-        return q;
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        int o = __ldg(a.offsets + e), c = __ldg(a.counts + e);
+        if (c < 0 || (c > 0 && (o < 0 || (int64_t)o + c > a.rows))) {
+            md::report(a.status, MD_ERR_DATA);
+            c = 0;
+        }
+        tab.off[e] = c > 0 ? o : 0;
+        tab.cnt[e] = c;
+        tab.order[e] = e;
     }
-    const int rt = t / mt;
-    const int mi = t - rt * mt;
-    int lo = 0, hi = a.E;  // last expert whose first tile is at or before rt
+}
+
+// Rows of a row tile of an expert with c rows: equal tiles of at most BN.
+template <int CG, int BN>
+__device__ __forceinline__ int tile_rows(int c)
+{
+    constexpr int kGran = 16 * CG;
+    const int nt = (c + BN - 1) / BN;
+    return nt ? ((c + nt - 1) / nt + kGran - 1) / kGran * kGran : 0;
+}
+
+// Order the experts by the cost of their tiles, falling (equal: by number), by
+// all threads; a barrier follows.  Tiles are dealt to the clusters back and
+// forth, so that the clusters' sums stay within a tile of each other and
+// the cheapest tiles come last.
+template <int MODE>
+__device__ __forceinline__ void sort_experts(const Table &tab, const Args &a)
+{
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
+        tab.pre[e] = MODE == kWgrad ? tab.cnt[e] : tile_rows<2, 256>(tab.cnt[e]);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        const int c = tab.pre[e];
+        int before = 0;
+        for (int o = 0; o < a.E; ++o) before += tab.pre[o] > c || (tab.pre[o] == c && o < e);
+        tab.order[before] = e;
+    }
+    __syncthreads();
+}
+
+// Exclusive running sum of the experts' row tiles, by one warp.
+template <int BN>
+__device__ __forceinline__ void count_tiles(const Table &tab, Shared *sh, const Args &a)
+{
+    const int lane = threadIdx.x & 31;
+    int run = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+        const int e = e0 + lane;
+        const int own = e < a.E ? (tab.cnt[tab.order[e]] + BN - 1) / BN : 0;
+        int v = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, v, d);
+            if (lane >= d) v += o;
+        }
+        if (e < a.E) tab.pre[e] = run + v - own;
+        run += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) sh->tiles = run;
+}
+
+// Rows of row tile rt.
+template <int CG, int BN>
+__device__ __forceinline__ Tile rows_at(int rt, const Table &tab, const Args &a)
+{
+    constexpr int kGran = 16 * CG;
+    int lo = 0, hi = a.E;  // last place in the order whose first tile is at or before rt
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (tab.pre[mid] <= rt) lo = mid;
         else hi = mid;
     }
-    const int c = tab.cnt[lo], nt = (c + BN - 1) / BN;
-    const int each = ((c + nt - 1) / nt + P::kGran - 1) / P::kGran * P::kGran;
-    const int at = (rt - tab.pre[lo]) * each;
-    q.e = lo;
-    q.m0 = (mi * CG + rank) * P::kMWidth;
-    q.r0 = (int64_t)tab.off[lo] + at;
+    Tile q;
+    q.e = tab.order[lo];
+    const int c = tab.cnt[q.e], each = tile_rows<CG, BN>(c), at = (rt - tab.pre[lo]) * each;
+    q.m0 = 0;
+    q.r0 = (int64_t)tab.off[q.e] + at;
     q.count = c - at < each ? c - at : each;
     q.c0 = 0;
-    q.n = (q.count + P::kGran - 1) / P::kGran * P::kGran;
+    q.n = (q.count + kGran - 1) / kGran * kGran;
     return q;
 }
 
@@ -180,6 +237,22 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// g / (1 + exp(-g)) * u.  exp(-g) = 2^t with t = -g log2(e); t's rounding error,
+// which would be |g| 2^-24 of the result, is put back to first order, so the result
+// is good to a few float32 ulps for |g| < 44 and to 2^-17 of itself beyond
+// (where exp overflows, it is 0).
+__device__ __forceinline__ float silu_times(float g, float u)
+{
+    constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+    const float t = -g * kLog2e;
+    const float lost = fabsf(t) < 64.0f ? fmaf(-g, kLog2e, -t) * kLn2 : 0.0f;
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    e = lost == 0.0f ? e : fmaf(e, lost, e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r * u;
 }
 
 // Eight columns of one row and one half of the checkpoint.  The four lanes of
@@ -218,27 +291,114 @@ __device__ __forceinline__ void pack_block(const float (&v)[8], bool valid, bool
     if (owner) *scale = (uint8_t)s;
 }
 
-template <int MODE, int CG, int BN>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_expert(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-             const __grid_constant__ CUtensorMap map_d, const __grid_constant__ Args a)
+// Output of 32 accumulator columns (x rows c .. c + 31 of the tile): v[i] is column c + i of
+// this thread's TMEM lane.  The group of four warps turns them around in its 8 KB staging
+// buffer (32 rows of 128 bf16, or twice 16 rows of 128 floats), so that global
+// stores are rows of 16-byte pieces.
+constexpr int kStagingBytes = 2 * 8192;
+
+template <int MODE>
+__device__ __forceinline__ void emit(const uint32_t (&v)[32], int c, const Tile &q, unsigned char *staging,
+                                     const Args &a)
 {
-    using P = Plan<MODE, CG, BN>;
-    static_assert(!P::kWg || CG == 1, "the pair's second CTA does not clear its share of a last block");
+    const int lane = threadIdx.x & 31, gw = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
+    const int row = threadIdx.x & 127;  // TMEM lane: weight row of the tile
+    const int live = q.count - c < 32 ? q.count - c : 32;
+    if (MODE != kGated) {
+        __nv_bfloat16 *st = reinterpret_cast<__nv_bfloat16 *>(staging + group * 8192);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) st[i * kTileM + row] = __float2bfloat16_rn(__uint_as_float(v[i]));
+        md::named_barrier(2 + group, 128);
+        const uint4 *src = reinterpret_cast<const uint4 *>(st);
+        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y);
+        const int n0 = q.m0 + (row & 15) * 8;
+        if (n0 < a.n)
+            for (int i = row >> 4; i < live; i += 8)
+                *reinterpret_cast<uint4 *>(y + (q.r0 + c + i) * a.pitch + n0) = src[i * 16 + (row & 15)];
+        md::named_barrier(2 + group, 128);  // the buffer is free again
+        return;
+    }
+    // lanes 0-63 of the tile hold g, 64-127 hold u of the same columns
+    float *st = reinterpret_cast<float *>(staging + group * 8192);
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+        if (h >= live) break;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st[i * kTileM + row] = __uint_as_float(v[h + i]);
+        md::named_barrier(2 + group, 128);
+        const int j = lane & 7, f0 = q.m0 + j * 8;
+        const bool valid = f0 < a.n;
+        const int i0 = gw * 4 + h;  // four rows to a warp
+        if (i0 < live) {
+            const bool in = i0 + (lane >> 3) < live;
+            const int ii = in ? i0 + (lane >> 3) : i0;
+            float g[8], u[8];
+            const float *at = st + (ii - h) * kTileM + j * 8;
+            *reinterpret_cast<float4 *>(g) = *reinterpret_cast<const float4 *>(at);
+            *reinterpret_cast<float4 *>(g + 4) = *reinterpret_cast<const float4 *>(at + 4);
+            *reinterpret_cast<float4 *>(u) = *reinterpret_cast<const float4 *>(at + 64);
+            *reinterpret_cast<float4 *>(u + 4) = *reinterpret_cast<const float4 *>(at + 68);
+            const int64_t r = q.r0 + c + ii;
+            if (a.codes) {
+                const int blocks = (a.n + kBlock - 1) / kBlock;
+                uint8_t *cr = a.codes + r * 2 * a.n + f0, *sr = a.scales + r * 2 * blocks + f0 / kBlock;
+                pack_block(g, valid, valid && in, cr, sr, (j & 3) == 0);
+                pack_block(u, valid, valid && in, cr + a.n, sr + blocks, (j & 3) == 0);
+            }
+            if (valid && in) {
+                uint32_t w[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    w[p] = md::pack_bf16x2(silu_times(g[2 * p], u[2 * p]), silu_times(g[2 * p + 1], u[2 * p + 1]));
+                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + r * a.pitch + f0) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        md::named_barrier(2 + group, 128);  // the buffer is free again
+    }
+}
+
+// ------------------------------------------------------- few rows to an expert
+//
+// Tiles of 128 weight rows by up to 64 x rows, one CTA each.  The time is that of
+// reading every chosen expert's weights once, so what counts is bytes in
+// flight: a ring of 8 stages keeps 128 KB of weights on the way to each SM.
+// Where there are too few tiles for the GPU (one token's eight experts), a cluster
+// of CTAs shares each tile's contraction: every CTA leaves its float32 part in its
+// ring's memory, and the first adds them in their order.
+template <int MODE>
+struct Few {
+    static constexpr int BN = 64, kStages = 8, kBox = 16;  // x rows per TMA box
+    static constexpr int kStageBytes = kABytes + BN * kTileK * 2;
+    static constexpr int kThreads = 32 * 10;
+    static constexpr int kWidth = MODE == kGated ? 64 : kTileM;  // output columns of a tile
+    static constexpr int kCols = 2 * BN;                         // TMEM columns: two accumulators
+    static size_t smem(int E) { return 1024 + (size_t)kStages * kStageBytes + kStagingBytes + Table::bytes(E); }
+};
+
+struct FewBars {
+    uint64_t full[8], empty[8], tfull[2], tempty[2], drain;
+};
+
+template <int MODE>
+__global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
+    k_expert_few(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                 const __grid_constant__ Args a)
+{
+    using P = Few<MODE>;
+    constexpr int BN = P::BN;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(16) Bars bars;
+    __shared__ Shared shared;
+    __shared__ __align__(16) FewBars bars;
+    Shared *sh = &shared;
+    FewBars *b = &bars;
     unsigned char *base = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *staging = base + P::kStages * P::kStageBytes;
-    Table tab;
-    tab.off = reinterpret_cast<int *>(staging + P::kStaging);
-    tab.cnt = tab.off + a.E;
-    tab.pre = tab.cnt + a.E;
+    const Table tab(staging + kStagingBytes, a.E);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = CG == 1 ? 0 : (int)md::cluster_rank();
-    Bars *b = &bars;
+    const int share = a.split > 1 ? (int)md::cluster_rank() : 0;  // of the contraction
 
-    // ---- setup: barriers, TMEM, the experts' ranges and tile counts
     if (threadIdx.x == 0) {
         for (int i = 0; i < P::kStages; ++i) {
             md::mbar_init(&b->full[i], 1);
@@ -246,346 +406,583 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             md::mbar_init(&b->tfull[i], 1);
-            md::mbar_init(&b->tempty[i], kEpiWarps * CG);
+            md::mbar_init(&b->tempty[i], kEpiWarps);
         }
         md::mbar_init(&b->drain, 1);
-        b->abort = 0;
+        sh->abort = 0;
         md::fence_mbar_init();
     }
-    if (warp == 4) {
-        if (lane == 0) {
-            md::prefetch_map(&map_a);
-            md::prefetch_map(&map_b);
-        }
+    if (warp == kLoadWarp && lane == 0) {
+        md::prefetch_map(&map_a);
+        md::prefetch_map(&map_b);
     }
-    if (warp == 5) md::tmem_alloc<CG>(&b->tmem, P::kCols);
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
-        int o = __ldg(a.offsets + e), c = __ldg(a.counts + e);
-        if (c < 0 || (c > 0 && (o < 0 || (int64_t)o + c > a.rows))) {
-            md::report(a.status, MD_ERR_DATA);
-            c = 0;
-        }
-        tab.off[e] = c > 0 ? o : 0;
-        tab.cnt[e] = c;
-    }
+    if (warp == kMmaWarp) md::tmem_alloc<1>(&sh->tmem, P::kCols);
+    read_ranges(tab, a);
     __syncthreads();
-    if (!P::kWg && warp == 0) {  // exclusive running sum of the experts' row tiles
-        int run = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane;
-            const int own = e < a.E ? (tab.cnt[e] + BN - 1) / BN : 0;
-            int v = own;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, v, d);
-                if (lane >= d) v += o;
-            }
-            if (e < a.E) tab.pre[e] = run + v - own;
-            run += __shfl_sync(0xffffffffu, v, 31);
-        }
-        if (lane == 0) b->tiles = run;
-    }
+    if (warp == 0) count_tiles<BN>(tab, sh, a);
     md::tmem_fence_before();
-    if (CG == 2) md::cluster_sync();
     __syncthreads();
     md::tmem_fence_after();
-    const uint32_t tmem = b->tmem;
+    const uint32_t tmem = sh->tmem;
 
-    const int mt = (a.n + P::kMWidth * CG - 1) / (P::kMWidth * CG);  // tiles along the weight rows
-    const int total = P::kWg ? a.E * mt * ((a.k + BN - 1) / BN) : b->tiles * mt;  // the host keeps it below 2^31
-    const int first = blockIdx.x / CG, step = gridDim.x / CG;
+    const int mt = (a.n + P::kWidth - 1) / P::kWidth;  // tiles along the weight rows
+    const int total = sh->tiles * mt;                  // the host keeps it below 2^30
+    const int first = blockIdx.x / a.split, step = gridDim.x / a.split;
     const uint32_t sbase = md::smem_addr(base);
+    // blocks of the contraction: [kb0, kb1) in this CTA
+    const int kblocks = (a.k + kTileK - 1) / kTileK;
+    const int kb0 = kblocks * share / a.split, kb1 = kblocks * (share + 1) / a.split;
+    auto tile_of = [&](int t) {
+        Tile q = rows_at<1, BN>(t / mt, tab, a);
+        q.m0 = t % mt * P::kWidth;
+        return q;
+    };
 
-    if (warp == 4) {
+    if (warp == kLoadWarp) {
         // ------------------------------------------------ loads
         if (lane == 0) {
-            Turn<P::kStages> at;
+            Turn at(P::kStages);
             int used = 0;  // stages loaded at least once
             bool ok = true;
             for (int t = first; ok && t < total; t += step) {
-                const Tile q = tile_at<MODE, CG, BN>(t, tab, a, mt, rank);
-                const int kb = P::kWg ? (q.count + kTileK - 1) / kTileK : (a.k + kTileK - 1) / kTileK;
-                const int half = q.n / CG;  // N-side lines of this CTA
-                const int boxes = P::kWg ? (half + 63) / 64 : (half + P::kBox - 1) / P::kBox;
-                const uint32_t bytes = (kABytes + boxes * (P::kWg ? 8192 : P::kBox * 128)) * CG;
-                const int r0 = (int)q.r0 + (P::kWg ? 0 : rank * half), c0 = q.c0 + rank * half;
-                for (int i = 0; i < kb; ++i) {
+                const Tile q = tile_of(t);
+                const int boxes = (q.n + P::kBox - 1) / P::kBox, r0 = (int)q.r0;
+                const uint32_t bytes = kABytes + boxes * P::kBox * 128;
+                for (int i = kb0; i < kb1; ++i) {
                     const int s = at.s;
-                    if (!wait_for(&b->empty[s], at.parity ^ 1u, b, a)) {
-                        ok = false;
-                        break;
-                    }
-                    uint32_t bar = md::smem_addr(&b->full[s]);
-                    if (rank == 0) md::mbar_expect_tx(&b->full[s], bytes);
-                    if (CG == 2) bar = md::map_rank(bar, 0);
+                    if (!(ok = wait_for(&b->empty[s], at.parity ^ 1u, sh, a))) break;
+                    const uint32_t bar = md::smem_addr(&b->full[s]);
+                    md::mbar_expect_tx(&b->full[s], bytes);
                     const uint32_t sa = sbase + s * P::kStageBytes, sb = sa + kABytes;
                     const int k0 = i * kTileK;
                     if (MODE == kNK) {
-                        md::tma_load_3d<CG>(sa, &map_a, k0, q.m0, q.e, bar);
+                        md::tma_load_3d<1>(sa, &map_a, k0, q.m0, q.e, bar);
                     } else if (MODE == kGated) {
-                        md::tma_load_3d<CG>(sa, &map_a, k0, q.m0, q.e, bar);
-                        md::tma_load_3d<CG>(sa + 8192, &map_a, k0, a.n + q.m0, q.e, bar);
-                    } else if (MODE == kKN) {
-                        md::tma_load_3d<CG>(sa, &map_a, q.m0, k0, q.e, bar);
-                        md::tma_load_3d<CG>(sa + 8192, &map_a, q.m0 + 64, k0, q.e, bar);
+                        md::tma_load_3d<1>(sa, &map_a, k0, q.m0, q.e, bar);
+                        md::tma_load_3d<1>(sa + 8192, &map_a, k0, a.n + q.m0, q.e, bar);
                     } else {
-                        md::tma_load_2d<CG>(sa, &map_a, q.m0, r0 + k0, bar);
-                        md::tma_load_2d<CG>(sa + 8192, &map_a, q.m0 + 64, r0 + k0, bar);
+                        md::tma_load_3d<1>(sa, &map_a, q.m0, k0, q.e, bar);
+                        md::tma_load_3d<1>(sa + 8192, &map_a, q.m0 + 64, k0, q.e, bar);
                     }
-                    for (int j = 0; j < boxes; ++j) {
-                        if (P::kWg) md::tma_load_2d<CG>(sb + j * 8192, &map_b, c0 + j * 64, r0 + k0, bar);
-                        else md::tma_load_2d<CG>(sb + j * P::kBox * 128, &map_b, k0, r0 + j * P::kBox, bar);
-                    }
+                    for (int j = 0; j < boxes; ++j)
+                        md::tma_load_2d<1>(sb + j * P::kBox * 128, &map_b, k0, r0 + j * P::kBox, bar);
                     if (used < P::kStages) ++used;
                     at.next();
                 }
             }
-            // await the copies in flight, whoever gave up: the last load of every stage
-            if (rank == 0) {
-                for (int j = 0; j < used; ++j) {  // backwards from the last stage loaded
-                    at.parity ^= at.s == 0 ? 1u : 0u;
-                    at.s = at.s == 0 ? P::kStages - 1 : at.s - 1;
-                    md::mbar_wait_bounded(&b->full[at.s], at.parity, kDrainPolls);
-                }
-            } else if (!ok) {
-                for (int j = 0; j < 2000; ++j) __nanosleep(500);
-            }
+            drain_loads(at, used, b->full);
         }
-    } else if (warp == 5) {
+    } else if (warp == kMmaWarp) {
         // ------------------------------------------------ products
-        if (rank == 0 && (P::kWg || lane == 0)) {
-            constexpr bool kAKMajor = MODE == kNK || MODE == kGated;
+        if (lane == 0) {
+            constexpr bool kAKMajor = MODE != kKN;
             const uint64_t da0 = kAKMajor ? md::operand_desc(sbase, 16, 1024) : md::operand_desc(sbase, 8192, 1024);
-            const uint64_t db0 = P::kWg ? md::operand_desc(sbase + kABytes, 8192, 1024)
-                                        : md::operand_desc(sbase + kABytes, 16, 1024);
-            constexpr int kAStep = (kAKMajor ? 32 : 2048) >> 4, kBStep = (P::kWg ? 2048 : 32) >> 4;
-            Turn<P::kStages> at;
+            const uint64_t db0 = md::operand_desc(sbase + kABytes, 16, 1024);
+            constexpr int kAStep = (kAKMajor ? 32 : 2048) >> 4;
+            Turn at(P::kStages);
             int acc = 0;
             bool ok = true;
-            for (int t = first; ok && t < total; t += step) {
-                const Tile q = tile_at<MODE, CG, BN>(t, tab, a, mt, rank);
-                const int kb = P::kWg ? (q.count + kTileK - 1) / kTileK : (a.k + kTileK - 1) / kTileK;
-                if (kb == 0) continue;
+            for (int t = first; ok && t < total; t += step, ++acc) {
+                const Tile q = tile_of(t);
                 const int buf = acc & 1;
-                const uint32_t idesc = md::mma_desc(kTileM * CG, q.n, !kAKMajor, P::kWg);
-                const uint32_t d = tmem + buf * BN;
-                const uint32_t tparity = (uint32_t)((acc >> 1) & 1) ^ 1u;
-                if (P::kWg ? !warp_wait(&b->tempty[buf], tparity, b, a) : !wait_for(&b->tempty[buf], tparity, b, a))
-                    break;
+                const uint32_t idesc = md::mma_desc(kTileM, q.n, !kAKMajor, false), d = tmem + buf * BN;
+                if (!wait_for(&b->tempty[buf], (uint32_t)((acc >> 1) & 1) ^ 1u, sh, a)) break;
                 md::tmem_fence_after();
-                ++acc;
-                for (int i = 0; i < kb; ++i) {
+                for (int i = kb0; i < kb1; ++i) {
                     const int s = at.s;
-                    int steps = kTileK / 16;
-                    if (P::kWg) {
-                        if (!warp_wait(&b->full[s], at.parity, b, a)) {
-                            ok = false;
-                            break;
-                        }
-                        // the last block reaches into the next expert's rows: rows past the end
-                        // are cleared on both sides (zero times a stray NaN or Inf is not zero)
-                        const int v = q.count - i * kTileK;
-                        if (v < kTileK) {
-                            steps = (v + 15) / 16;
-                            const int boxes = 2 + (q.n / CG + 63) / 64;
-                            const int lines = steps * 16 - v, n16 = lines * 8 * boxes;
-                            for (int z = lane; z < n16; z += 32) {
-                                const int box = z / (lines * 8), w = z - box * (lines * 8);
-                                *reinterpret_cast<uint4 *>(base + s * P::kStageBytes + box * 8192 + (v + (w >> 3)) * 128 +
-                                                           (w & 7) * 16) = make_uint4(0, 0, 0, 0);
-                            }
-                            md::fence_async_shared();
-                            __syncwarp();
-                        }
-                    } else if (!wait_for(&b->full[s], at.parity, b, a)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!(ok = wait_for(&b->full[s], at.parity, sh, a))) break;
                     md::tmem_fence_after();
-                    if (lane == 0) {
-                        const uint64_t da = da0 + (uint32_t)(s * (P::kStageBytes >> 4));
-                        const uint64_t db = db0 + (uint32_t)(s * (P::kStageBytes >> 4));
+                    const uint64_t da = da0 + (uint32_t)(s * (P::kStageBytes >> 4));
+                    const uint64_t db = db0 + (uint32_t)(s * (P::kStageBytes >> 4));
 #pragma unroll
-                        for (int j = 0; j < kTileK / 16; ++j)
-                            if (!P::kWg || j < steps)
-                                md::mma_bf16<CG>(d, da + j * kAStep, db + j * kBStep, idesc, i > 0 || j > 0);
-                        md::mma_commit<CG>(&b->empty[s]);
-                        if (i == kb - 1) md::mma_commit<CG>(&b->tfull[buf]);
-                    }
-                    if (P::kWg) __syncwarp();
+                    for (int j = 0; j < kTileK / 16; ++j)
+                        md::mma_bf16<1>(d, da + j * kAStep, db + j * 2, idesc, i > kb0 || j > 0);
+                    md::mma_commit<1>(&b->empty[s]);
+                    if (i == kb1 - 1) md::mma_commit<1>(&b->tfull[buf]);
                     at.next();
                 }
             }
-            if (lane == 0) {  // await the MMAs in flight, whoever gave up
-                md::mma_commit<CG>(&b->drain);
-                md::mbar_wait_bounded(&b->drain, 0, kDrainPolls);
+            md::mma_commit<1>(&b->drain);  // await the MMAs in flight, whoever gave up
+            md::mbar_wait_bounded(&b->drain, 0, kDrainPolls);
+        }
+    } else {
+        // ------------------------------------------------ results
+        int acc = 0;
+        const int group = warp >> 2;
+        const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+        for (int t = first; t < total; t += step, ++acc) {
+            const Tile q = tile_of(t);
+            const int buf = acc & 1;
+            if (!epilogue_wait(&b->tfull[buf], (uint32_t)((acc >> 1) & 1), sh, a)) break;
+            md::tmem_fence_after();
+            const int c = group * 32;
+            uint32_t v[32];
+            if (c < q.count) {
+                md::tmem_ld32(v, tmem + quarter + buf * BN + c);
+                md::tmem_ld_wait();
+            }
+            md::tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) md::mbar_arrive(&b->tempty[buf]);
+            if (c >= q.count) continue;
+            if (a.split > 1) {  // left in the ring's memory, which this cluster's one tile is done with
+                float *pt = reinterpret_cast<float *>(base);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (c + i < q.count) pt[(c + i) * kTileM + (threadIdx.x & 127)] = __uint_as_float(v[i]);
+            } else {
+                emit<MODE>(v, c, q, staging, a);
+            }
+        }
+    }
+
+    if (a.split > 1) {
+        __syncwarp();
+        __syncthreads();
+        md::cluster_sync();
+        if (share == 0 && warp < kEpiWarps && first < total) {
+            const Tile q = tile_of(first);
+            const int c = (warp >> 2) * 32;
+            if (c < q.count) {
+                uint32_t v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0;
+                for (int p = 0; p < a.split; ++p) {
+                    const uint32_t from = md::map_rank(sbase + (c * kTileM + (threadIdx.x & 127)) * 4, p);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (c + i < q.count)
+                            v[i] = __float_as_uint(__uint_as_float(v[i]) + md::ld_cluster(from + i * kTileM * 4));
+                }
+                emit<MODE>(v, c, q, staging, a);
+            }
+        }
+    }
+
+    // ---- end: nobody leaves while its cluster may still read its shared memory
+    __syncwarp();
+    md::tmem_fence_before();
+    __syncthreads();
+    if (a.split > 1) md::cluster_sync();
+    md::tmem_fence_after();
+    if (warp == kMmaWarp) md::tmem_free<1>(tmem, P::kCols);
+}
+
+// ------------------------------------------------------ many rows to an expert
+//
+// A pair of CTAs makes 512 weight rows by up to 256 x rows (weight gradient: by 256
+// columns): two M = 256 products ("subs") that share each block of x.  Every block of 64 of
+// the contraction then brings 48 KB into an SM for 1024 tensor-core cycles.  What
+// bounds this form is that path: about 45 bytes a cycle reach an SM from L2 when
+// all of them load, and one 256 x 256 product per block needs 64 (it measured 70%
+// of the tensor cores' rate; two need 47).  Calls with too few such tiles for the
+// GPU take one sub.
+//
+// A stage holds a block of sub 0's A, of x, and of sub 1's A, on one barrier, and
+// A and x have a loading thread each: a thread's instructions around a barrier and
+// its copies took longer than the products when one thread did it all.
+//
+// The two accumulators of 256 columns fill TMEM and are used in turn, one for
+// each (tile, sub).  The epilogue's warps take an accumulator into registers and
+// free it before most of it is written out, and at a tile's first and last blocks
+// the subs go two blocks at a time, so that each accumulator has 1024 cycles to be
+// freed while the other sub works.  For that the epilogue's warps hold up to 216
+// registers: 12 warps of 168 at launch, 8 x 216 + 4 x 72 after.
+//
+// Weight gradient.  The contraction runs over an expert's rows, and its last block
+// reaches into the next expert's: rows past the end are cleared in shared memory
+// on both sides (zero times a stray NaN or Inf is not zero), by the MMA warp of
+// each CTA, so there every CTA awaits its own loads, and the second CTA
+// passes each stage on to the first.  The tensor cores drop low bits at each
+// addition: over thousands of rows the sums drift by 1.6e-6.  float32 results are
+// therefore summed in TMEM over kSegment blocks at most and then added in dw.
+constexpr int kSegment = 32;
+
+template <int MODE>
+struct Wide {
+    static constexpr int kPart = 128 * kTileK * 2;  // 16 KB: 128 rows of A, or half of the tile's x rows
+    static constexpr int kParts = 12;               // 4 stages of three, or 6 of two (one sub)
+    static constexpr int kThreads = 32 * 12;
+    static constexpr int kSub = MODE == kGated ? 128 : 256;  // output columns of a sub
+    static size_t smem(int E) { return 1024 + (size_t)kParts * kPart + kStagingBytes + Table::bytes(E); }
+};
+
+struct WideBars {
+    uint64_t full[6], empty[6], tfull[2], tempty[2], drain;
+};
+
+// Blocks that the subs take at a time from block i on.
+__device__ __forceinline__ int blocks_at(int i, int kb, int subs)
+{
+    return subs == 2 && kb - i >= 2 && (i == 0 || i == kb - 2) ? 2 : 1;
+}
+
+// 32 columns of this thread's row of dw, straight from registers: float32 in
+// whole 32-byte sectors (if dw is aligned so), bf16 in halves of one.
+__device__ __forceinline__ void put_row(const uint32_t (&v)[32], const Args &a, int64_t at, int live, bool add)
+{
+    if (a.out_bf16) {
+        uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (8 * i < live) {
+                uint32_t w[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    w[h] = md::pack_bf16x2(__uint_as_float(v[8 * i + 2 * h]), __uint_as_float(v[8 * i + 2 * h + 1]));
+                p[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        return;
+    }
+    float *p = static_cast<float *>(a.y) + at;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (8 * i < live) {
+            float f[8];
+#pragma unroll
+            for (int h = 0; h < 8; ++h) f[h] = __uint_as_float(v[8 * i + h]);
+            if (add) {
+                const float4 lo = *reinterpret_cast<const float4 *>(p + 8 * i), hi = *reinterpret_cast<const float4 *>(p + 8 * i + 4);
+                f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
+                f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
+            }
+            if (a.sectors) {
+                md::st_sector(p + 8 * i, f);
+            } else {
+                *reinterpret_cast<float4 *>(p + 8 * i) = make_float4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<float4 *>(p + 8 * i + 4) = make_float4(f[4], f[5], f[6], f[7]);
+            }
+        }
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
+    k_expert_wide(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                  const __grid_constant__ Args a)
+{
+    using W = Wide<MODE>;
+    constexpr int BN = 256;
+    constexpr bool kWg = MODE == kWgrad;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ Shared shared;
+    __shared__ __align__(16) WideBars bars;
+    Shared *sh = &shared;
+    WideBars *b = &bars;
+    unsigned char *base = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char *staging = base + W::kParts * W::kPart;
+    const Table tab(staging + kStagingBytes, a.E);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)md::cluster_rank();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 6; ++i) {
+            // two loading threads; weight gradient: and the second CTA's word to the first
+            md::mbar_init(&b->full[i], kWg && rank == 0 ? 3 : 2);
+            md::mbar_init(&b->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            md::mbar_init(&b->tfull[i], 1);
+            md::mbar_init(&b->tempty[i], kEpiWarps * 2);
+        }
+        md::mbar_init(&b->drain, 1);
+        sh->abort = 0;
+        md::fence_mbar_init();
+    }
+    if (warp == kLoadWarp && lane == 0) md::prefetch_map(&map_a);
+    if (warp == kLoadXWarp && lane == 0) md::prefetch_map(&map_b);
+    if (warp == kMmaWarp) md::tmem_alloc<2>(&sh->tmem, 512);
+    read_ranges(tab, a);
+    __syncthreads();
+    sort_experts<MODE>(tab, a);
+    if (!kWg && warp == 0) count_tiles<BN>(tab, sh, a);
+    md::tmem_fence_before();
+    md::cluster_sync();
+    __syncthreads();
+    md::tmem_fence_after();
+    const uint32_t tmem = sh->tmem;
+
+    const int width = a.subs * W::kSub;  // output columns (weight gradient: rows of dw) of a tile
+    const int mt = (a.n + width - 1) / width, ct = (a.k + BN - 1) / BN;
+    const int total = kWg ? a.E * mt * ct : sh->tiles * mt;  // the host keeps it below 2^30
+    const int step = gridDim.x / 2, place = blockIdx.x / 2, rounds = (total + step - 1) / step;
+    // the cluster's tile of a round, dealt back and forth; `total` or more: none
+    auto deal = [&](int round) { return round * step + (round & 1 ? step - 1 - place : place); };
+    const uint32_t sbase = md::smem_addr(base);
+    const int stages = W::kParts / (a.subs + 1), stage_bytes = (a.subs + 1) * W::kPart;
+    auto tile_of = [&](int t) {
+        Tile q;
+        if (kWg) {
+            const int per = mt * ct, at = t / per, i = t - at * per, ci = i / mt;
+            q.e = tab.order[at];
+            q.r0 = tab.off[q.e];
+            q.count = tab.cnt[q.e];
+            q.c0 = ci * BN;
+            q.n = (min(a.k - q.c0, BN) + 31) / 32 * 32;
+        } else {
+            q = rows_at<2, BN>(t / mt, tab, a);
+        }
+        q.m0 = t % mt * width + rank * (W::kSub / 2);
+        return q;
+    };
+    // the last tile along the weight rows may have one sub where others have two
+    auto subs_of = [&](int t) { return a.subs == 2 && t % mt * width + W::kSub < a.n ? 2 : 1; };
+    // blocks of the tile's contraction
+    auto blocks_of = [&](const Tile &q) { return ((kWg ? q.count : a.k) + kTileK - 1) / kTileK; };
+    // blocks that one accumulator sums
+    const int segment = kWg && !a.out_bf16 ? kSegment : INT32_MAX;
+
+    if (warp >= kEpiWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == kLoadWarp || warp == kLoadXWarp) {
+            // ------------------------------------------------ loads
+            if (lane == 0) {
+                constexpr int kTma = kWg ? 1 : 2;         // weight gradient: each CTA awaits its own loads
+                const bool own_bar = kWg || rank == 0;    // else the first CTA's barrier counts them
+                Turn at(stages);
+                int used = 0;  // stages loaded at least once
+                bool ok = true;
+                for (int round = 0; ok && round < rounds; ++round) {
+                    const int t = deal(round);
+                    if (t >= total) continue;
+                    const Tile q = tile_of(t);
+                    const int subs = subs_of(t), kb = blocks_of(q);
+                    const int half = q.n / 2, boxes = (half + 63) / 64;  // N-side lines of this CTA
+                    const int r0 = (int)q.r0 + (kWg ? 0 : rank * half), c0 = q.c0 + rank * half;
+                    const uint32_t bytes = kTma * (warp == kLoadWarp ? subs * W::kPart : boxes * 8192);
+                    for (int i = 0; i < kb; ++i) {
+                        if (!(ok = wait_for(&b->empty[at.s], at.parity ^ 1u, sh, a))) break;
+                        uint32_t bar = md::smem_addr(&b->full[at.s]);
+                        if (own_bar) md::mbar_expect_tx(&b->full[at.s], bytes);
+                        else bar = md::map_rank(bar, 0);
+                        const uint32_t to = sbase + at.s * stage_bytes;
+                        const int k0 = i * kTileK;
+                        if (warp == kLoadXWarp) {
+                            for (int j = 0; j < boxes; ++j) {
+                                const uint32_t tx = to + W::kPart + j * 8192;
+                                if (kWg) md::tma_load_2d<kTma>(tx, &map_b, c0 + j * 64, r0 + k0, bar);
+                                else md::tma_load_2d<kTma>(tx, &map_b, k0, r0 + j * 64, bar);
+                            }
+                        } else {
+                            for (int sub = 0; sub < subs; ++sub) {
+                                const uint32_t ta = to + sub * 2 * W::kPart;
+                                const int m = q.m0 + sub * W::kSub;
+                                if (MODE == kNK) {
+                                    md::tma_load_3d<kTma>(ta, &map_a, k0, m, q.e, bar);
+                                } else if (MODE == kGated) {
+                                    md::tma_load_3d<kTma>(ta, &map_a, k0, m, q.e, bar);
+                                    md::tma_load_3d<kTma>(ta + 8192, &map_a, k0, a.n + m, q.e, bar);
+                                } else if (MODE == kKN) {
+                                    md::tma_load_3d<kTma>(ta, &map_a, m, k0, q.e, bar);
+                                    md::tma_load_3d<kTma>(ta + 8192, &map_a, m + 64, k0, q.e, bar);
+                                } else {
+                                    md::tma_load_2d<kTma>(ta, &map_a, m, r0 + k0, bar);
+                                    md::tma_load_2d<kTma>(ta + 8192, &map_a, m + 64, r0 + k0, bar);
+                                }
+                            }
+                        }
+                        if (used < stages) ++used;
+                        at.next();
+                    }
+                }
+                if (own_bar) drain_loads(at, used, b->full);
+                else if (!ok)
+                    for (int j = 0; j < 2000; ++j) __nanosleep(500);
+            }
+        } else if (warp == kMmaWarp) {
+            // ------------------------------------------------ products
+            if (kWg || (rank == 0 && lane == 0)) {
+                constexpr bool kAKMajor = MODE == kNK || MODE == kGated;
+                const uint64_t da0 = kAKMajor ? md::operand_desc(sbase, 16, 1024) : md::operand_desc(sbase, 8192, 1024);
+                const uint64_t db0 = kWg ? md::operand_desc(sbase, 8192, 1024) : md::operand_desc(sbase, 16, 1024);
+                constexpr int kAStep = (kAKMajor ? 32 : 2048) >> 4, kBStep = (kWg ? 2048 : 32) >> 4;
+                Turn at(stages);
+                uint32_t opened = 0;  // accumulators taken so far
+                bool ok = true;
+                for (int round = 0; ok && round < rounds; ++round) {
+                    const int t = deal(round);
+                    if (t >= total) continue;
+                    const Tile q = tile_of(t);
+                    const int subs = subs_of(t), blocks = blocks_of(q);
+                    const uint32_t idesc = md::mma_desc(256, q.n, !kAKMajor, kWg);
+                    for (int from = 0, kb; ok && from < blocks; from += kb, opened += subs) {
+                        kb = min(blocks - from, segment);
+                        // block i of one sub, in stage s, the first `steps` sixteenths of it
+                        auto product = [&](int sub, int i, int s, int steps) {
+                            const uint32_t acc = opened + sub;
+                            if (i == 0) {
+                                const uint32_t parity = ((acc >> 1) & 1u) ^ 1u;
+                                if (kWg ? !warp_wait(&b->tempty[acc & 1], parity, sh, a) : !wait_for(&b->tempty[acc & 1], parity, sh, a))
+                                    return false;
+                                md::tmem_fence_after();
+                            }
+                            if (kWg && lane != 0) return true;
+                            const uint32_t off = (uint32_t)(s * stage_bytes) >> 4;
+                            const uint64_t da = da0 + off + (sub ? 2 * W::kPart >> 4 : 0), db = db0 + off + (W::kPart >> 4);
+    #pragma unroll
+                            for (int j = 0; j < kTileK / 16; ++j)
+                                if (!kWg || j < steps)
+                                    md::mma_bf16<2>(tmem + (acc & 1) * BN, da + j * kAStep, db + j * kBStep, idesc, i > 0 || j > 0);
+                            if (sub == subs - 1) md::mma_commit<2>(&b->empty[s]);
+                            if (i == kb - 1) md::mma_commit<2>(&b->tfull[acc & 1]);
+                            return true;
+                        };
+                        for (int i = 0, g; ok && i < kb; i += g) {
+                            g = blocks_at(i, kb, subs);
+                            int s[2], steps[2];
+                            for (int j = 0; ok && j < g; ++j) {
+                                s[j] = at.s;
+                                steps[j] = kTileK / 16;
+                                if (!(ok = kWg ? warp_wait(&b->full[at.s], at.parity, sh, a) : wait_for(&b->full[at.s], at.parity, sh, a)))
+                                    break;
+                                if (kWg) {
+                                    const int v = q.count - (from + i + j) * kTileK;  // rows left
+                                    if (v < kTileK) {
+                                        steps[j] = (v + 15) / 16;
+                                        const int boxes = 2 + (q.n / 2 + 63) / 64 + (subs == 2 ? 2 : 0);
+                                        const int lines = steps[j] * 16 - v, n16 = lines * 8 * boxes;
+                                        for (int z = lane; z < n16; z += 32) {
+                                            int box = z / (lines * 8);
+                                            const int w = z - box * (lines * 8);
+                                            if (box >= 2 + (q.n / 2 + 63) / 64) box += 2 - (q.n / 2 + 63) / 64;  // sub 1's A
+                                            *reinterpret_cast<uint4 *>(base + at.s * stage_bytes + box * 8192 +
+                                                                       (v + (w >> 3)) * 128 + (w & 7) * 16) = make_uint4(0, 0, 0, 0);
+                                        }
+                                        md::fence_async_shared();
+                                        if (rank == 1) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                                        __syncwarp();
+                                    }
+                                    // the second CTA's word to the first: loaded and cleared.  Relaxed: a
+                                    // release at each stage took longer than the stage's products, and
+                                    // only cleared stages have writes of this warp to order.
+                                    if (rank == 1 && lane == 0)
+                                        md::mbar_arrive_cluster_relaxed(md::map_rank(md::smem_addr(&b->full[at.s]), 0));
+                                }
+                                md::tmem_fence_after();
+                                at.next();
+                                if (!kWg || rank == 0) ok = product(0, i + j, s[j], steps[j]);
+                            }
+                            if (!kWg || rank == 0)
+                                for (int j = 0; ok && subs == 2 && j < g; ++j) ok = product(1, i + j, s[j], steps[j]);
+                        }
+                    }
+                }
+                if (rank == 0 && lane == 0) {  // await the MMAs in flight, whoever gave up
+                    md::mma_commit<2>(&b->drain);
+                    md::mbar_wait_bounded(&b->drain, 0, kDrainPolls);
+                }
             }
         }
     } else {
         // ------------------------------------------------ results
-        int acc = 0, chunk = 0;
-        const uint32_t quarter = (uint32_t)(warp * 32) << 16;
-        for (int t = first; t < total; t += step) {
-            const Tile q = tile_at<MODE, CG, BN>(t, tab, a, mt, rank);
-            const bool zero = P::kWg && q.count == 0;
-            if (zero && a.accumulate) continue;
-            const int buf = acc & 1;
-            if (!zero) {
-                if (!all_warps(warp_wait(&b->tfull[buf], (uint32_t)((acc >> 1) & 1), b, a))) break;
-                md::tmem_fence_after();
-                ++acc;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int group = warp >> 2;
+        const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + group * 32;
+        uint32_t acc = 0;
+        bool ok = true;
+        // this warp's columns of an accumulator, in four runs of 32, into registers (all of them,
+        // the tile's or not: a register that is loaded on a condition stays taken throughout)
+        auto take = [&](uint32_t (&v)[4][32]) __attribute__((always_inline)) {
+            ok = epilogue_wait(&b->tfull[acc & 1], (acc >> 1) & 1u, sh, a);
+            if (!ok) return;
+            md::tmem_fence_after();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) md::tmem_ld32(v[i], mine + (acc & 1) * BN + i * 64);
+            md::tmem_ld_wait();
+            md::tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) md::mbar_arrive_cluster(md::map_rank(md::smem_addr(&b->tempty[acc & 1]), 0));
+            ++acc;
+        };
+        // the subs' accumulators, out through put(values, sub, run).  Sub 1's is taken when half of
+        // sub 0's registers are free again.
+        auto results = [&](int subs, auto put) __attribute__((always_inline)) {
+            uint32_t v[4][32];
+            take(v);
+            if (!ok) return;
+            put(v[0], 0, 0);
+            put(v[1], 0, 1);
+            if (subs == 2) {
+                uint32_t w[4][32];
+                take(w);
+                if (!ok) return;
+                put(v[2], 0, 2);
+                put(v[3], 0, 3);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) put(w[i], 1, i);
+            } else {
+                put(v[2], 0, 2);
+                put(v[3], 0, 3);
             }
-            const uint32_t d = tmem + quarter + buf * BN;
-            if (P::kWg) {
-                // this warp's 32 rows of dw, 128 bytes of columns at a time
-                const int wide = a.out_bf16 ? 64 : 32;
-                const int left = a.k - q.c0, cols = left < BN ? left : BN;
-                const int n0 = q.m0 + warp * 32;
-                for (int c = 0; c < cols; c += wide, ++chunk) {
-                    uint32_t v[32], w[32];
-                    if (!zero) {
-                        md::tmem_ld32(v, d + c);
-                        if (a.out_bf16) md::tmem_ld32(w, d + c + 32);
-                        md::tmem_ld_wait();
-                        if (a.out_bf16) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                v[i] = md::pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                                w[i] = md::pack_bf16x2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-                            }
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) v[16 + i] = w[i];
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0;
+        };
+        for (int round = 0; ok && round < rounds; ++round) {
+            const int t = deal(round);
+            if (t >= total) continue;
+            const Tile q = tile_of(t);
+            const int subs = subs_of(t);
+            if (kWg) {
+                const int blocks = blocks_of(q), cols = min(a.k - q.c0, BN);
+                if (blocks == 0 && a.accumulate) continue;
+                for (int from = 0; from == 0 || (ok && from < blocks); from += min(segment, max(blocks - from, 1))) {
+                    const bool add = a.accumulate || from > 0;
+                    auto put = [&](const uint32_t (&x)[32], int sub, int i) __attribute__((always_inline)) {
+                        const int c = group * 32 + i * 64, row = q.m0 + sub * W::kSub + (threadIdx.x & 127);
+                        if (c < cols && row < a.n)
+                            put_row(x, a, ((int64_t)q.e * a.n + row) * a.k + q.c0 + c, cols - c, add);
+                    };
+                    if (blocks == 0) {
+                        uint32_t none[32] = {};
+                        for (int sub = 0; sub < subs; ++sub)
+                            for (int i = 0; i < 4; ++i) put(none, sub, i);
+                        break;
                     }
-                    unsigned char *st = staging + warp * 8192 + (chunk & 1) * 4096;
-                    if (lane == 0) md::bulk_wait_read<1>();  // the store that read this buffer
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)  // the map's 128-byte swizzle
-                        *reinterpret_cast<uint4 *>(st + lane * 128 + ((i ^ (lane & 7)) * 16)) =
-                            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    md::fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (n0 < a.n) {
-                            if (a.accumulate) md::tma_add_3d(&map_d, md::smem_addr(st), q.c0 + c, n0, q.e);
-                            else md::tma_store_3d(&map_d, md::smem_addr(st), q.c0 + c, n0, q.e);
-                        }
-                        md::bulk_commit();
-                    }
+                    results(subs, put);
                 }
             } else {
-                for (int c = 0; c < q.count; c += 32, ++chunk) {
-                    uint32_t v[32];
-                    md::tmem_ld32(v, d + c);
-                    md::tmem_ld_wait();
-                    const int live = q.count - c < 32 ? q.count - c : 32;
-                    if (MODE != kGated) {
-                        // lane = weight row: lines of 32 x rows by 128 weight rows
-                        __nv_bfloat16 *st = reinterpret_cast<__nv_bfloat16 *>(staging + (chunk & 1) * 8192);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            st[i * kTileM + threadIdx.x] = __float2bfloat16_rn(__uint_as_float(v[i]));
-                        md::named_barrier(1, kEpiWarps * 32);
-                        const uint4 *src = reinterpret_cast<const uint4 *>(st);
-                        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y);
-                        const int n0 = q.m0 + (threadIdx.x & 15) * 8;
-                        if (n0 < a.n)
-                            for (int i = threadIdx.x >> 4; i < live; i += 8)
-                                *reinterpret_cast<uint4 *>(y + (q.r0 + c + i) * a.pitch + n0) =
-                                    src[i * 16 + (threadIdx.x & 15)];
-                    } else {
-                        // lanes 0-63 of the tile hold g, 64-127 hold u of the same columns
-                        float *st = reinterpret_cast<float *>(staging + (chunk & 1) * 16384);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) st[i * kTileM + threadIdx.x] = __uint_as_float(v[i]);
-                        md::named_barrier(1, kEpiWarps * 32);
-                        const int j = threadIdx.x & 7, f0 = q.m0 + j * 8;
-                        const bool valid = f0 < a.n;
-                        for (int i0 = warp * 4; i0 < live; i0 += 16) {  // four rows to a warp
-                            const bool in = i0 + (lane >> 3) < live;
-                            const int ii = in ? i0 + (lane >> 3) : i0;
-                            float g[8], u[8];
-                            *reinterpret_cast<float4 *>(g) = *reinterpret_cast<const float4 *>(st + ii * kTileM + j * 8);
-                            *reinterpret_cast<float4 *>(g + 4) = *reinterpret_cast<const float4 *>(st + ii * kTileM + j * 8 + 4);
-                            *reinterpret_cast<float4 *>(u) = *reinterpret_cast<const float4 *>(st + ii * kTileM + 64 + j * 8);
-                            *reinterpret_cast<float4 *>(u + 4) = *reinterpret_cast<const float4 *>(st + ii * kTileM + 64 + j * 8 + 4);
-                            const int64_t r = q.r0 + c + ii;
-                            if (a.codes) {
-                                const int blocks = (a.n + kBlock - 1) / kBlock;
-                                uint8_t *cr = a.codes + r * 2 * a.n + f0, *sr = a.scales + r * 2 * blocks + f0 / kBlock;
-                                pack_block(g, valid, valid && in, cr, sr, (j & 3) == 0);
-                                pack_block(u, valid, valid && in, cr + a.n, sr + blocks, (j & 3) == 0);
-                            }
-                            if (valid && in) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int p = 0; p < 4; ++p) {
-                                    const float x0 = g[2 * p] / (1.0f + expf(-g[2 * p])) * u[2 * p];
-                                    const float x1 = g[2 * p + 1] / (1.0f + expf(-g[2 * p + 1])) * u[2 * p + 1];
-                                    w[p] = md::pack_bf16x2(x0, x1);
-                                }
-                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + r * a.pitch + f0) =
-                                    make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        }
-                    }
-                }
-            }
-            if (!zero) {
-                md::tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 1) md::mbar_arrive(&b->tempty[buf]);
-                    else md::mbar_arrive_cluster(md::map_rank(md::smem_addr(&b->tempty[buf]), 0));
-                }
+                auto put = [&](const uint32_t (&x)[32], int sub, int i) __attribute__((always_inline)) {
+                    Tile at = q;
+                    at.m0 += sub * W::kSub;
+                    if (group * 32 + i * 64 < q.count) emit<MODE>(x, group * 32 + i * 64, at, staging, a);
+                };
+                results(subs, put);
             }
         }
-        if (P::kWg && lane == 0) md::bulk_wait_all();
     }
 
     // ---- end: nobody leaves while its pair may still read its shared memory
     __syncwarp();
     md::tmem_fence_before();
     __syncthreads();
-    if (CG == 2) md::cluster_sync();
+    md::cluster_sync();
     md::tmem_fence_after();
-    if (warp == 5) md::tmem_free<CG>(tmem, P::kCols);
+    if (warp == kMmaWarp) md::tmem_free<2>(tmem, 512);
 }
 
 // ------------------------------------------------------------------ host
 
-// One launch; the caller has made the maps.
-template <int MODE, int CG, int BN>
-int launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md_, Args &a, int64_t tiles,
-           cudaStream_t s)
+// One launch in clusters of `members` CTAs.
+template <class Kernel>
+int launch(Kernel kernel, int threads, size_t smem, size_t most_smem, std::atomic<uint64_t> &setup, int64_t clusters,
+           int members, const CUtensorMap &ma, const CUtensorMap &mb, const Args &a, cudaStream_t s)
 {
-    using P = Plan<MODE, CG, BN>;
-    if (tiles > (int64_t)1 << 30) return MD_ERR_UNSUPPORTED;
-    static std::atomic<uint64_t> setup{0};
-    md::once_per_device(setup, [] {
-        if (cudaFuncSetAttribute(k_expert<MODE, CG, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)P::smem(MD_MAX_EXPERTS)) != cudaSuccess)
+    md::once_per_device(setup, [&] {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem) != cudaSuccess)
             cudaGetLastError();  // the launch then fails and reports MD_ERR_CUDA
     });
-    const int64_t most = md::sm_count() / CG;
-    const int64_t grid = (tiles < 1 ? 1 : tiles < most ? tiles : most) * CG;
+    const int64_t most = md::sm_count() / members;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = P::smem(a.E);
+    cfg.gridDim = dim3((unsigned)((clusters < most ? clusters : most) * members));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CG;
+    at[0].val.clusterDim.x = members;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k_expert<MODE, CG, BN>, ma, mb, md_, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernel, ma, mb, a) != cudaSuccess) {
         cudaGetLastError();
         return MD_ERR_CUDA;
     }
@@ -594,7 +991,6 @@ int launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md_,
 }
 
 constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-constexpr CUtensorMapDataType kF32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
 
 bool bad_sizes(int64_t rows, int E, int N, int K)
 {
@@ -609,22 +1005,52 @@ bool too_large(int64_t rows, int E, int64_t N, int64_t K)
            N * K > ((int64_t)1 << 37);
 }
 
-// gemm (w_layout) and gated share everything but the A operand's boxes.
-template <int MODE, int CG, int BN>
-int run_rows(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int64_t d1, cudaStream_t s)
+constexpr int64_t kMostTiles = (int64_t)1 << 30;
+
+template <int MODE>
+int run_few(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int64_t d1, cudaStream_t s)
 {
-    using P = Plan<MODE, CG, BN>;
+    using P = Few<MODE>;
     CUtensorMap ma, mb;
     if (!md::make_map(&ma, w, kBf16, 2, d0, d1, a.E, 64, MODE == kNK ? kTileM : 64) ||
         !md::make_map(&mb, x, kBf16, 2, a.k, rows, 0, 64, P::kBox))
         return MD_ERR_CUDA;
-    const int mt = (a.n + P::kMWidth * CG - 1) / (P::kMWidth * CG);
-    const int64_t tiles = (rows / BN + (rows < a.E ? rows : a.E)) * mt;  // at most
-    return launch<MODE, CG, BN>(ma, mb, mb, a, tiles, s);
+    const int mt = (a.n + P::kWidth - 1) / P::kWidth;
+    const int64_t tiles = (rows / P::BN + (rows < a.E ? rows : a.E)) * mt;  // at most
+    if (tiles > kMostTiles) return MD_ERR_UNSUPPORTED;
+    // Few tiles leave SMs idle and each tile streams its weights through one SM: clusters of
+    // CTAs share a tile's contraction, as long as all of them are resident and each has
+    // four blocks or more.
+    a.split = 1;
+    while (a.split < kMaxSplit && tiles * a.split * 2 <= md::sm_count() && a.k >= a.split * 2 * 4 * kTileK)
+        a.split *= 2;
+    static std::atomic<uint64_t> setup{0};
+    return launch(k_expert_few<MODE>, P::kThreads, P::smem(a.E), P::smem(MD_MAX_EXPERTS), setup, tiles, a.split, ma, mb,
+                  a, s);
+}
+
+// Two subs to a tile where that still gives every pair of SMs several tiles.
+inline int subs_for(int64_t tiles_of_one) { return tiles_of_one >= 4 * md::sm_count() ? 2 : 1; }
+
+template <int MODE>
+int run_wide(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int64_t d1, cudaStream_t s)
+{
+    using W = Wide<MODE>;
+    CUtensorMap ma, mb;
+    if (!md::make_map(&ma, w, kBf16, 2, d0, d1, a.E, 64, MODE == kNK ? kTileM : 64) ||
+        !md::make_map(&mb, x, kBf16, 2, a.k, rows, 0, 64, 64))
+        return MD_ERR_CUDA;
+    const int64_t row_tiles = rows / 256 + (rows < a.E ? rows : a.E);  // at most
+    a.subs = subs_for(row_tiles * ((a.n + W::kSub - 1) / W::kSub));
+    const int mt = (a.n + a.subs * W::kSub - 1) / (a.subs * W::kSub);
+    if (row_tiles * mt > kMostTiles) return MD_ERR_UNSUPPORTED;
+    static std::atomic<uint64_t> setup{0};
+    return launch(k_expert_wide<MODE>, W::kThreads, W::smem(a.E), W::smem(MD_MAX_EXPERTS), setup, row_tiles * mt, 2, ma,
+                  mb, a, s);
 }
 
 // Few rows to an expert: narrow tiles leave shared memory for a deep ring,
-// since such a call is bound by reading the weights.  Many: 256-row tiles.
+// since such a call is bound by reading the weights.  Many: k_expert_wide.
 bool few_rows(int64_t rows, int E) { return rows <= (int64_t)48 * E; }
 
 }  // namespace
@@ -641,6 +1067,7 @@ extern "C" int md_expert_gemm(const void *x, int64_t rows, int K, const void *w,
     const int rc = md::clear_status(dev_status, s);
     if (rc != MD_OK || rows == 0) return rc;
     Args a = {};
+    a.split = 1;
     a.offsets = expert_offsets;
     a.counts = expert_counts;
     a.rows = rows;
@@ -652,10 +1079,10 @@ extern "C" int md_expert_gemm(const void *x, int64_t rows, int K, const void *w,
     a.status = dev_status;
     a.polls = md::hook_poll_limit(kPolls);
     if (w_layout == MD_W_NK)
-        return few_rows(rows, E) ? run_rows<kNK, 1, 64>(x, w, rows, a, K, N, s)
-                                 : run_rows<kNK, 2, 256>(x, w, rows, a, K, N, s);
-    return few_rows(rows, E) ? run_rows<kKN, 1, 64>(x, w, rows, a, N, K, s)
-                             : run_rows<kKN, 2, 256>(x, w, rows, a, N, K, s);
+        return few_rows(rows, E) ? run_few<kNK>(x, w, rows, a, K, N, s)
+                                 : run_wide<kNK>(x, w, rows, a, K, N, s);
+    return few_rows(rows, E) ? run_few<kKN>(x, w, rows, a, N, K, s)
+                             : run_wide<kKN>(x, w, rows, a, N, K, s);
 }
 
 extern "C" int md_expert_gated(const void *x, int64_t rows, int K, const void *w, int E, int F,
@@ -671,6 +1098,7 @@ extern "C" int md_expert_gated(const void *x, int64_t rows, int K, const void *w
     const int rc = md::clear_status(dev_status, s);
     if (rc != MD_OK || rows == 0) return rc;
     Args a = {};
+    a.split = 1;
     a.offsets = expert_offsets;
     a.counts = expert_counts;
     a.rows = rows;
@@ -683,8 +1111,8 @@ extern "C" int md_expert_gated(const void *x, int64_t rows, int K, const void *w
     a.scales = scales;
     a.status = dev_status;
     a.polls = md::hook_poll_limit(kPolls);
-    return few_rows(rows, E) ? run_rows<kGated, 1, 64>(x, w, rows, a, K, 2 * (int64_t)F, s)
-                             : run_rows<kGated, 2, 256>(x, w, rows, a, K, 2 * (int64_t)F, s);
+    return few_rows(rows, E) ? run_few<kGated>(x, w, rows, a, K, 2 * (int64_t)F, s)
+                             : run_wide<kGated>(x, w, rows, a, K, 2 * (int64_t)F, s);
 }
 
 extern "C" int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int E, int N, int K,
@@ -706,6 +1134,7 @@ extern "C" int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int 
         return cudaMemsetAsync(dw, 0, (size_t)E * N * K * size, s) == cudaSuccess ? MD_OK : MD_ERR_CUDA;
     }
     Args a = {};
+    a.split = 1;
     a.offsets = expert_offsets;
     a.counts = expert_counts;
     a.rows = rows;
@@ -714,12 +1143,18 @@ extern "C" int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int 
     a.k = K;
     a.out_bf16 = out_type == MD_BF16;
     a.accumulate = accumulate != 0;
+    a.sectors = (reinterpret_cast<uintptr_t>(dw) & 31u) == 0;
     a.status = dev_status;
     a.polls = md::hook_poll_limit(kPolls);
-    CUtensorMap ma, mb, mo;
-    if (!md::make_map(&ma, dy, kBf16, 2, N, rows, 0, 64, 64) || !md::make_map(&mb, x, kBf16, 2, K, rows, 0, 64, 64) ||
-        !md::make_map(&mo, dw, a.out_bf16 ? kBf16 : kF32, size, K, N, E, 128 / size, 32))
+    a.y = dw;
+    using W = Wide<kWgrad>;
+    CUtensorMap ma, mb;
+    if (!md::make_map(&ma, dy, kBf16, 2, N, rows, 0, 64, 64) || !md::make_map(&mb, x, kBf16, 2, K, rows, 0, 64, 64))
         return MD_ERR_CUDA;
-    const int64_t tiles = (int64_t)E * ((N + kTileM - 1) / kTileM) * ((K + 255) / 256);
-    return launch<kWgrad, 1, 256>(ma, mb, mo, a, tiles, s);
+    const int64_t across = (K + 255) / 256;
+    a.subs = subs_for(E * across * ((N + W::kSub - 1) / W::kSub));
+    const int64_t tiles = E * across * ((N + a.subs * W::kSub - 1) / (a.subs * W::kSub));
+    if (tiles > kMostTiles) return MD_ERR_UNSUPPORTED;
+    static std::atomic<uint64_t> setup{0};
+    return launch(k_expert_wide<kWgrad>, W::kThreads, W::smem(E), W::smem(MD_MAX_EXPERTS), setup, tiles, 2, ma, mb, a, s);
 }

@@ -177,6 +177,71 @@ def test_wgrad_accumulates_and_clears():
     assert torch.equal(dw.double(), want)
 
 
+def test_wgrad_into_a_buffer_of_16_byte_alignment():
+    counts, N, K = [70, 0, 33], 136, 264
+    off, cnt, rows, spans = groups(counts)
+    dy, x = ints(1, rows, N), ints(2, rows, K)
+    want = md.md_expert_wgrad(dy, x, off, cnt)
+    for shift in (4, 8):
+        flat = torch.full((3 * N * K + 16,), 9.0, device=DEV)
+        dw = flat[shift:shift + 3 * N * K].view(3, N, K)
+        md.md_expert_wgrad(dy, x, off, cnt, dw=dw)
+        assert torch.equal(dw, want)
+        assert bool((flat[:shift] == 9.0).all()) and bool((flat[shift + 3 * N * K:] == 9.0).all())
+
+
+@pytest.mark.parametrize("counts", [[2049], [5000, 0, 2048, 100]])
+def test_wgrad_of_long_experts(counts):
+    """Experts whose rows are summed in several parts, into a fresh and a kept dw."""
+    N, K = 264, 520
+    off, cnt, rows, spans = groups(counts, seed=5)
+    dy, x = ints(1, rows, N, hi=2), ints(2, rows, K, hi=2)
+    want = torch.zeros(len(counts), N, K, dtype=torch.float64, device=DEV)
+    for e, o, c in spans:
+        want[e] = dy[o:o + c].double().t() @ x[o:o + c].double()
+    dw = md.md_expert_wgrad(dy, x, off, cnt)
+    assert torch.equal(dw.double(), want)
+    md.md_expert_wgrad(dy, x, off, cnt, dw=dw, accumulate=True)
+    assert torch.equal(dw.double(), 2 * want)
+    assert torch.equal(md.md_expert_wgrad(dy, x, off, cnt, out_dtype=torch.bfloat16), want.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("op", ["nk", "kn", "gated", "wgrad"])
+def test_many_tiles_of_two_products(op):
+    """Enough tiles that each takes 512 weight rows, some of whose second halves are partly or
+    wholly outside; skewed counts."""
+    counts = [0, 700, 1, 256, 257, 513, 90, 33, 1200, 0, 64, 300, 129, 511, 512, 31]
+    K, N = 328, 1416
+    off, cnt, rows, spans = groups(counts, seed=8, gap=1)
+    E = len(counts)
+    x = ints(1, rows, K, hi=2)
+    if op == "wgrad":
+        dy = ints(2, rows, N, hi=2)
+        want = torch.zeros(E, N, K, dtype=torch.float64, device=DEV)
+        for e, o, c in spans:
+            want[e] = dy[o:o + c].double().t() @ x[o:o + c].double()
+        assert torch.equal(md.md_expert_wgrad(dy, x, off, cnt).double(), want)
+        return
+    mine = owned(rows, spans)
+    if op == "gated":
+        w = randn(2, E, 2 * N, K, scale=1.5 / 16)
+        got = md.md_expert_gated(x, w, off, cnt)
+        h, mags = products64(x, w, spans)
+        g, u = h.chunk(2, 1)
+        mg, mu = mags.chunk(2, 1)
+        want = g * torch.sigmoid(g) * u
+        tol = 2.0 ** -8 * want.abs() + K * 2.0 ** -23 * (1.1 * mg * u.abs() + mu * g.abs()) * 1.01 \
+            + 8 * 2.0 ** -23 * want.abs() + 1e-37
+        bad = ((got.double() - want).abs() > tol) & mine[:, None]
+        assert not bool(bad.any()), int(bad.sum())
+        return
+    nk = op == "nk"
+    w = ints(2, *((E, N, K) if nk else (E, K, N)), hi=1)
+    y = md.md_expert_gemm(x, w, off, cnt, md.MD_W_NK if nk else md.MD_W_KN)
+    want, _ = products64(x, w, spans, nk)
+    assert torch.equal(y[mine], want[mine].to(torch.bfloat16))
+
+
 # ------------------------------------------------------------------ gated, checkpoint
 
 def stored64(h):
