@@ -48,7 +48,7 @@ struct Args {
     int pitch;    // columns of y, or of a
     void *y;      // gemm: bf16 [rows, N]; gated: bf16 [rows, F]; wgrad: dw
     uint8_t *codes, *scales;  // gated: checkpoint or NULL
-    int out_bf16, accumulate, sectors;  // wgrad; sectors: dw is 32-byte aligned
+    int out_bf16, accumulate; // wgrad
     int subs;     // k_expert_wide: M = 256 products to a tile, at most
     int split;    // k_expert_few: CTAs (a cluster) that share each tile's contraction; each cluster has one tile
     int32_t *status;
@@ -617,42 +617,69 @@ __device__ __forceinline__ int blocks_at(int i, int kb, int subs)
     return subs == 2 && kb - i >= 2 && (i == 0 || i == kb - 2) ? 2 : 1;
 }
 
-// 32 columns of this thread's row of dw, straight from registers: float32 in
-// whole 32-byte sectors (if dw is aligned so), bf16 in halves of one.
-__device__ __forceinline__ void put_row(const uint32_t (&v)[32], const Args &a, int64_t at, int live, bool add)
+// 32 columns from column c on of dw's rows row0 .. row0 + 31, one row in each lane of
+// the warp, turned around in the warp's 2 KB of staging (swizzled: no bank is hit
+// twice) so that global accesses are whole 128-byte lines (bf16: halves).
+// Straight from registers, a row to a lane, each store touched 32 lines and
+// the stores took as long as 2048 rows' products.
+__device__ __forceinline__ void put_rows(const uint32_t (&v)[32], const Args &a, int e, int row0, int c, bool add,
+                                         unsigned char *st)
 {
+    const int lane = threadIdx.x & 31;
+    const int64_t first = ((int64_t)e * a.n + row0) * a.k + c;  // rows below it: 32-bit offsets
     if (a.out_bf16) {
-        uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + at);
+        const int sw = (lane >> 1 & 3) * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (8 * i < live) {
-                uint32_t w[4];
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
 #pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    w[h] = md::pack_bf16x2(__uint_as_float(v[8 * i + 2 * h]), __uint_as_float(v[8 * i + 2 * h + 1]));
-                p[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        return;
-    }
-    float *p = static_cast<float *>(a.y) + at;
+            for (int h = 0; h < 4; ++h)
+                w[h] = md::pack_bf16x2(__uint_as_float(v[8 * i + 2 * h]), __uint_as_float(v[8 * i + 2 * h + 1]));
+            *reinterpret_cast<uint4 *>(st + lane * 64 + (i * 16 ^ sw)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+        const int p = lane & 3;
+        if (c + p * 8 < a.k) {
+            __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.y) + first + p * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (8 * i < live) {
-            float f[8];
-#pragma unroll
-            for (int h = 0; h < 8; ++h) f[h] = __uint_as_float(v[8 * i + h]);
-            if (add) {
-                const float4 lo = *reinterpret_cast<const float4 *>(p + 8 * i), hi = *reinterpret_cast<const float4 *>(p + 8 * i + 4);
-                f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
-                f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
-            }
-            if (a.sectors) {
-                md::st_sector(p + 8 * i, f);
-            } else {
-                *reinterpret_cast<float4 *>(p + 8 * i) = make_float4(f[0], f[1], f[2], f[3]);
-                *reinterpret_cast<float4 *>(p + 8 * i + 4) = make_float4(f[4], f[5], f[6], f[7]);
+            for (int j = 0; j < 4; ++j) {
+                const int r = j * 8 + (lane >> 2);
+                if (row0 + r < a.n)
+                    *reinterpret_cast<uint4 *>(to + r * a.k) =
+                        *reinterpret_cast<const uint4 *>(st + r * 64 + (p * 16 ^ (r >> 1 & 3) * 16));
             }
         }
+        __syncwarp();
+        return;
+    }
+    const int p = lane & 7, sw = p * 16;
+    float *to = static_cast<float *>(a.y) + first + p * 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // 16 rows at a time
+        if (lane >> 4 == h) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4 *>(st + (lane & 15) * 128 + (i * 16 ^ sw)) =
+                    make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+        __syncwarp();
+        if (c + p * 4 < a.k) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = j * 4 + (lane >> 3);
+                if (row0 + h * 16 + r < a.n) {
+                    float4 f = *reinterpret_cast<const float4 *>(st + r * 128 + (sw ^ (r & 7) * 16));
+                    float4 *at = reinterpret_cast<float4 *>(to + (h * 16 + r) * a.k);
+                    if (add) {
+                        const float4 o = *at;
+                        f = make_float4(o.x + f.x, o.y + f.y, o.z + f.z, o.w + f.w);
+                    }
+                    *at = f;
+                }
+            }
+        }
+        __syncwarp();
+    }
 }
 
 template <int MODE>
@@ -877,7 +904,10 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
         // ------------------------------------------------ results
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int group = warp >> 2;
-        const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + group * 32;
+        // a group's runs of 32 columns: every other one, so that a short tile's are shared;
+        // weight gradient: adjacent ones, which are adjacent in dw
+        constexpr int kRun = kWg ? 32 : 64;
+        const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + group * (kWg ? 128 : 32);
         uint32_t acc = 0;
         bool ok = true;
         // this warp's columns of an accumulator, in four runs of 32, into registers (all of them,
@@ -887,13 +917,16 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
             if (!ok) return;
             md::tmem_fence_after();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) md::tmem_ld32(v[i], mine + (acc & 1) * BN + i * 64);
+            for (int i = 0; i < 4; ++i) md::tmem_ld32(v[i], mine + (acc & 1) * BN + i * kRun);
             md::tmem_ld_wait();
             md::tmem_fence_before();
             __syncwarp();
-            if (lane == 0) md::mbar_arrive_cluster(md::map_rank(md::smem_addr(&b->tempty[acc & 1]), 0));
+            // relaxed: what must be done are the reads of TMEM, and those are waited for; a release
+            // would wait for this warp's stores to global memory too
+            if (lane == 0) md::mbar_arrive_cluster_relaxed(md::map_rank(md::smem_addr(&b->tempty[acc & 1]), 0));
             ++acc;
         };
+        constexpr bool kThree = kWg || MODE == kGated;  // their put needs more registers
         // the subs' accumulators, out through put(values, sub, run).  Sub 1's is taken when half of
         // sub 0's registers are free again.
         auto results = [&](int subs, auto put) __attribute__((always_inline)) {
@@ -902,16 +935,17 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
             if (!ok) return;
             put(v[0], 0, 0);
             put(v[1], 0, 1);
+            if (kThree) put(v[2], 0, 2);
             if (subs == 2) {
                 uint32_t w[4][32];
                 take(w);
                 if (!ok) return;
-                put(v[2], 0, 2);
+                if (!kThree) put(v[2], 0, 2);
                 put(v[3], 0, 3);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) put(w[i], 1, i);
             } else {
-                put(v[2], 0, 2);
+                if (!kThree) put(v[2], 0, 2);
                 put(v[3], 0, 3);
             }
         };
@@ -926,9 +960,8 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                 for (int from = 0; from == 0 || (ok && from < blocks); from += min(segment, max(blocks - from, 1))) {
                     const bool add = a.accumulate || from > 0;
                     auto put = [&](const uint32_t (&x)[32], int sub, int i) __attribute__((always_inline)) {
-                        const int c = group * 32 + i * 64, row = q.m0 + sub * W::kSub + (threadIdx.x & 127);
-                        if (c < cols && row < a.n)
-                            put_row(x, a, ((int64_t)q.e * a.n + row) * a.k + q.c0 + c, cols - c, add);
+                        const int c = group * 128 + i * 32, row0 = q.m0 + sub * W::kSub + (warp & 3) * 32;
+                        if (c < cols && row0 < a.n) put_rows(x, a, q.e, row0, q.c0 + c, add, staging + warp * 2048);
                     };
                     if (blocks == 0) {
                         uint32_t none[32] = {};
@@ -1143,7 +1176,6 @@ extern "C" int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int 
     a.k = K;
     a.out_bf16 = out_type == MD_BF16;
     a.accumulate = accumulate != 0;
-    a.sectors = (reinterpret_cast<uintptr_t>(dw) & 31u) == 0;
     a.status = dev_status;
     a.polls = md::hook_poll_limit(kPolls);
     a.y = dw;

@@ -84,14 +84,6 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t addr)
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-// eight floats to a 32-byte aligned address
-__device__ __forceinline__ void st_sector(float *p, const float (&f)[8])
-{
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),
-                 "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
-                 : "memory");
-}
-
 // a float at a shared::cluster address
 __device__ __forceinline__ float ld_cluster(uint32_t addr)
 {
