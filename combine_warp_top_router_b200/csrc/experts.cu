@@ -62,26 +62,20 @@ struct Shared {
     int tiles;  // ragged row tiles of all experts
 };
 
-// Bounded wait of one thread; on run-out raises the CTA's abort flag.
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, Shared *sh, const Args &a)
-{
-    if (md::mbar_try_wait(bar, parity)) return true;
-    volatile int *ab = &sh->abort;
-    for (long long i = 1; i < a.polls; ++i) {
-        if (*ab) return false;
-        if (md::mbar_try_wait(bar, parity)) return true;
-    }
-    *ab = 1;
-    md::report(a.status, MD_ERR_TIMEOUT);
-    return false;
-}
-
-// The same for a whole warp: lane 0 waits, all lanes get its answer.
+// Bounded wait of a converged warp; all lanes get the same answer.  The first look
+// does not sleep, the others may.  On run-out raises the CTA's abort flag.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Shared *sh, const Args &a)
 {
-    int ok = 0;
-    if ((threadIdx.x & 31) == 0) ok = wait_for(bar, parity, sh, a);
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    if (__all_sync(0xffffffffu, md::mbar_test_wait(bar, parity))) return true;
+    volatile int *ab = &sh->abort;
+    for (long long i = 1; i < a.polls; ++i) {
+        if (__any_sync(0xffffffffu, *ab)) return false;
+        if (__all_sync(0xffffffffu, md::mbar_try_wait(bar, parity))) return true;
+    }
+    *ab = 1;
+    if ((threadIdx.x & 31) == 0) md::report(a.status, MD_ERR_TIMEOUT);
+    __syncwarp();
+    return false;
 }
 
 // Wait of the epilogue's warps: the first polls, the others sleep at a barrier,
@@ -440,7 +434,7 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------ loads
-        if (lane == 0) {
+        {
             Turn at(P::kStages);
             int used = 0;  // stages loaded at least once
             bool ok = true;
@@ -450,9 +444,9 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
                 const uint32_t bytes = kABytes + boxes * P::kBox * 128;
                 for (int i = kb0; i < kb1; ++i) {
                     const int s = at.s;
-                    if (!(ok = wait_for(&b->empty[s], at.parity ^ 1u, sh, a))) break;
+                    if (!(ok = warp_wait(&b->empty[s], at.parity ^ 1u, sh, a))) break;
                     const uint32_t bar = md::smem_addr(&b->full[s]);
-                    md::mbar_expect_tx(&b->full[s], bytes);
+                    md::expect_tx_one(&b->full[s], bytes);
                     const uint32_t sa = sbase + s * P::kStageBytes, sb = sa + kABytes;
                     const int k0 = i * kTileK;
                     if (MODE == kNK) {
@@ -474,7 +468,7 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------ products
-        if (lane == 0) {
+        {
             constexpr bool kAKMajor = MODE != kKN;
             const uint64_t da0 = kAKMajor ? md::operand_desc(sbase, 16, 1024) : md::operand_desc(sbase, 8192, 1024);
             const uint64_t db0 = md::operand_desc(sbase + kABytes, 16, 1024);
@@ -486,11 +480,11 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
                 const Tile q = tile_of(t);
                 const int buf = acc & 1;
                 const uint32_t idesc = md::mma_desc(kTileM, q.n, !kAKMajor, false), d = tmem + buf * BN;
-                if (!wait_for(&b->tempty[buf], (uint32_t)((acc >> 1) & 1) ^ 1u, sh, a)) break;
+                if (!warp_wait(&b->tempty[buf], (uint32_t)((acc >> 1) & 1) ^ 1u, sh, a)) break;
                 md::tmem_fence_after();
                 for (int i = kb0; i < kb1; ++i) {
                     const int s = at.s;
-                    if (!(ok = wait_for(&b->full[s], at.parity, sh, a))) break;
+                    if (!(ok = warp_wait(&b->full[s], at.parity, sh, a))) break;
                     md::tmem_fence_after();
                     const uint64_t da = da0 + (uint32_t)(s * (P::kStageBytes >> 4));
                     const uint64_t db = db0 + (uint32_t)(s * (P::kStageBytes >> 4));
@@ -592,8 +586,9 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
 // Weight gradient.  The contraction runs over an expert's rows, and its last block
 // reaches into the next expert's: rows past the end are cleared in shared memory
 // on both sides (zero times a stray NaN or Inf is not zero), by the MMA warp of
-// each CTA, so there every CTA awaits its own loads, and the second CTA
-// passes each stage on to the first.  The tensor cores drop low bits at each
+// each CTA.  For such a block the second CTA awaits its loads on a barrier of
+// its own, clears, and tells the first; passing every stage on this way took a
+// quarter of the loads' rate.  The tensor cores drop low bits at each
 // addition: over thousands of rows the sums drift by 1.6e-6.  float32 results are
 // therefore summed in TMEM over kSegment blocks at most and then added in dw.
 constexpr int kSegment = 32;
@@ -609,6 +604,10 @@ struct Wide {
 
 struct WideBars {
     uint64_t full[6], empty[6], tfull[2], tempty[2], drain;
+    // Weight gradient, a tile's last block in stage s: loaded (second CTA's barrier), and cleared
+    // there (first CTA's).  One for each stage, since the loads run tiles ahead of
+    // the products where tiles are short; roles keep their parities in a bit for each.
+    uint64_t tail[6], cleared[6];
 };
 
 // Blocks that the subs take at a time from block i on.
@@ -704,9 +703,10 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 6; ++i) {
-            // two loading threads; weight gradient: and the second CTA's word to the first
-            md::mbar_init(&b->full[i], kWg && rank == 0 ? 3 : 2);
+            md::mbar_init(&b->full[i], 2);  // the first CTA's two loading threads
             md::mbar_init(&b->empty[i], 1);
+            md::mbar_init(&b->tail[i], 2);
+            md::mbar_init(&b->cleared[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             md::mbar_init(&b->tfull[i], 1);
@@ -763,11 +763,10 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kLoadWarp || warp == kLoadXWarp) {
             // ------------------------------------------------ loads
-            if (lane == 0) {
-                constexpr int kTma = kWg ? 1 : 2;         // weight gradient: each CTA awaits its own loads
-                const bool own_bar = kWg || rank == 0;    // else the first CTA's barrier counts them
+            {
                 Turn at(stages);
                 int used = 0;  // stages loaded at least once
+                uint32_t tails = 0, used_tails = 0;
                 bool ok = true;
                 for (int round = 0; ok && round < rounds; ++round) {
                     const int t = deal(round);
@@ -776,35 +775,43 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                     const int subs = subs_of(t), kb = blocks_of(q);
                     const int half = q.n / 2, boxes = (half + 63) / 64;  // N-side lines of this CTA
                     const int r0 = (int)q.r0 + (kWg ? 0 : rank * half), c0 = q.c0 + rank * half;
-                    const uint32_t bytes = kTma * (warp == kLoadWarp ? subs * W::kPart : boxes * 8192);
+                    const uint32_t bytes = warp == kLoadWarp ? subs * W::kPart : boxes * 8192;
                     for (int i = 0; i < kb; ++i) {
-                        if (!(ok = wait_for(&b->empty[at.s], at.parity ^ 1u, sh, a))) break;
-                        uint32_t bar = md::smem_addr(&b->full[at.s]);
-                        if (own_bar) md::mbar_expect_tx(&b->full[at.s], bytes);
-                        else bar = md::map_rank(bar, 0);
+                        if (!(ok = warp_wait(&b->empty[at.s], at.parity ^ 1u, sh, a))) break;
+                        // the first CTA's barrier counts both CTAs' bytes, but for a block to be cleared
+                        const bool tail = kWg && i == kb - 1 && q.count % kTileK != 0;
+                        uint32_t bar = md::map_rank(md::smem_addr(&b->full[at.s]), 0);
+                        if (rank == 0) {
+                            md::expect_tx_one(&b->full[at.s], tail ? bytes : 2 * bytes);
+                        } else if (tail) {
+                            md::expect_tx_one(&b->tail[at.s], bytes);
+                            bar = md::map_rank(md::smem_addr(&b->tail[at.s]), 1);
+                            used_tails |= 1u << at.s;
+                            tails ^= 1u << at.s;
+                        }
                         const uint32_t to = sbase + at.s * stage_bytes;
                         const int k0 = i * kTileK;
                         if (warp == kLoadXWarp) {
                             for (int j = 0; j < boxes; ++j) {
                                 const uint32_t tx = to + W::kPart + j * 8192;
-                                if (kWg) md::tma_load_2d<kTma>(tx, &map_b, c0 + j * 64, r0 + k0, bar);
-                                else md::tma_load_2d<kTma>(tx, &map_b, k0, r0 + j * 64, bar);
+                                if (kWg) md::tma_load_2d<2>(tx, &map_b, c0 + j * 64, r0 + k0, bar);
+                                else md::tma_load_2d<2>(tx, &map_b, k0, r0 + j * 64, bar);
                             }
                         } else {
                             for (int sub = 0; sub < subs; ++sub) {
                                 const uint32_t ta = to + sub * 2 * W::kPart;
                                 const int m = q.m0 + sub * W::kSub;
                                 if (MODE == kNK) {
-                                    md::tma_load_3d<kTma>(ta, &map_a, k0, m, q.e, bar);
+                                    md::tma_load_3d<2>(ta, &map_a, k0, m, q.e, bar);
                                 } else if (MODE == kGated) {
-                                    md::tma_load_3d<kTma>(ta, &map_a, k0, m, q.e, bar);
-                                    md::tma_load_3d<kTma>(ta + 8192, &map_a, k0, a.n + m, q.e, bar);
+                                    md::tma_load_3d<2>(ta, &map_a, k0, m, q.e, bar);
+                                    md::tma_load_3d<2>(ta + 8192, &map_a, k0, a.n + m, q.e, bar);
                                 } else if (MODE == kKN) {
-                                    md::tma_load_3d<kTma>(ta, &map_a, m, k0, q.e, bar);
-                                    md::tma_load_3d<kTma>(ta + 8192, &map_a, m + 64, k0, q.e, bar);
+                                    md::tma_load_3d<2>(ta, &map_a, m, k0, q.e, bar);
+                                    md::tma_load_3d<2>(ta + 8192, &map_a, m + 64, k0, q.e, bar);
                                 } else {
-                                    md::tma_load_2d<kTma>(ta, &map_a, m, r0 + k0, bar);
-                                    md::tma_load_2d<kTma>(ta + 8192, &map_a, m + 64, r0 + k0, bar);
+                                    md::tma_load_2d<2>(ta, &map_a, m, r0 + k0, bar);
+                                    md::tma_load_2d<2>(ta + 8192, &map_a, m + 64, r0 + k0, bar);
                                 }
                             }
                         }
@@ -812,17 +819,51 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                         at.next();
                     }
                 }
-                if (own_bar) drain_loads(at, used, b->full);
-                else if (!ok)
+                if (rank == 0) drain_loads(at, used, b->full);
+                else
+                    for (int i = 0; i < stages; ++i)
+                        if (used_tails >> i & 1u) md::mbar_wait_bounded(&b->tail[i], (tails >> i & 1u) ^ 1u, kDrainPolls);
+                if (rank == 1 && !ok)
                     for (int j = 0; j < 2000; ++j) __nanosleep(500);
             }
         } else if (warp == kMmaWarp) {
             // ------------------------------------------------ products
-            if (kWg || (rank == 0 && lane == 0)) {
+            // Clears the lines from v on, up to the last of `steps` sixteenths, of every box of a stage.
+            auto clear = [&](int s, int v, int steps, int xboxes, int subs) {
+                const int boxes = 2 + xboxes + (subs == 2 ? 2 : 0), lines = steps * 16 - v;
+                for (int z = lane; z < lines * 8 * boxes; z += 32) {
+                    int box = z / (lines * 8);
+                    const int w = z - box * (lines * 8);
+                    if (box >= 2 + xboxes) box += 2 - xboxes;  // sub 1's A, behind x's two boxes
+                    *reinterpret_cast<uint4 *>(base + s * stage_bytes + box * 8192 + (v + (w >> 3)) * 128 + (w & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                md::fence_async_shared();
+                __syncwarp();
+            };
+            uint32_t tails = 0;
+            if (kWg && rank == 1) {
+                Turn at(stages);
+                for (int round = 0; round < rounds; ++round) {
+                    const int t = deal(round);
+                    if (t >= total) continue;
+                    const Tile q = tile_of(t);
+                    for (int i = 0; i < blocks_of(q); ++i) at.next();
+                    const int v = q.count % kTileK;
+                    if (v == 0) continue;
+                    at.back();
+                    if (!warp_wait(&b->tail[at.s], tails >> at.s & 1u, sh, a)) break;
+                    tails ^= 1u << at.s;
+                    clear(at.s, v, (v + 15) / 16, (q.n / 2 + 63) / 64, subs_of(t));
+                    if (lane == 0) md::mbar_arrive_cluster(md::map_rank(md::smem_addr(&b->cleared[at.s]), 0));
+                    at.next();
+                }
+            } else if (rank == 0) {
                 constexpr bool kAKMajor = MODE == kNK || MODE == kGated;
                 const uint64_t da0 = kAKMajor ? md::operand_desc(sbase, 16, 1024) : md::operand_desc(sbase, 8192, 1024);
                 const uint64_t db0 = kWg ? md::operand_desc(sbase, 8192, 1024) : md::operand_desc(sbase, 16, 1024);
                 constexpr int kAStep = (kAKMajor ? 32 : 2048) >> 4, kBStep = (kWg ? 2048 : 32) >> 4;
+                auto await = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, sh, a); };
                 Turn at(stages);
                 uint32_t opened = 0;  // accumulators taken so far
                 bool ok = true;
@@ -838,18 +879,20 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                         auto product = [&](int sub, int i, int s, int steps) {
                             const uint32_t acc = opened + sub;
                             if (i == 0) {
-                                const uint32_t parity = ((acc >> 1) & 1u) ^ 1u;
-                                if (kWg ? !warp_wait(&b->tempty[acc & 1], parity, sh, a) : !wait_for(&b->tempty[acc & 1], parity, sh, a))
-                                    return false;
+                                if (!await(&b->tempty[acc & 1], ((acc >> 1) & 1u) ^ 1u)) return false;
                                 md::tmem_fence_after();
                             }
-                            if (kWg && lane != 0) return true;
                             const uint32_t off = (uint32_t)(s * stage_bytes) >> 4;
                             const uint64_t da = da0 + off + (sub ? 2 * W::kPart >> 4 : 0), db = db0 + off + (W::kPart >> 4);
-    #pragma unroll
-                            for (int j = 0; j < kTileK / 16; ++j)
-                                if (!kWg || j < steps)
+                            if (!kWg || steps == kTileK / 16) {
+#pragma unroll
+                                for (int j = 0; j < kTileK / 16; ++j)
                                     md::mma_bf16<2>(tmem + (acc & 1) * BN, da + j * kAStep, db + j * kBStep, idesc, i > 0 || j > 0);
+                            } else {
+#pragma unroll 1
+                                for (int j = 0; j < steps; ++j)
+                                    md::mma_bf16<2>(tmem + (acc & 1) * BN, da + j * kAStep, db + j * kBStep, idesc, i > 0 || j > 0);
+                            }
                             if (sub == subs - 1) md::mma_commit<2>(&b->empty[s]);
                             if (i == kb - 1) md::mma_commit<2>(&b->tfull[acc & 1]);
                             return true;
@@ -860,44 +903,24 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                             for (int j = 0; ok && j < g; ++j) {
                                 s[j] = at.s;
                                 steps[j] = kTileK / 16;
-                                if (!(ok = kWg ? warp_wait(&b->full[at.s], at.parity, sh, a) : wait_for(&b->full[at.s], at.parity, sh, a)))
-                                    break;
-                                if (kWg) {
-                                    const int v = q.count - (from + i + j) * kTileK;  // rows left
-                                    if (v < kTileK) {
-                                        steps[j] = (v + 15) / 16;
-                                        const int boxes = 2 + (q.n / 2 + 63) / 64 + (subs == 2 ? 2 : 0);
-                                        const int lines = steps[j] * 16 - v, n16 = lines * 8 * boxes;
-                                        for (int z = lane; z < n16; z += 32) {
-                                            int box = z / (lines * 8);
-                                            const int w = z - box * (lines * 8);
-                                            if (box >= 2 + (q.n / 2 + 63) / 64) box += 2 - (q.n / 2 + 63) / 64;  // sub 1's A
-                                            *reinterpret_cast<uint4 *>(base + at.s * stage_bytes + box * 8192 +
-                                                                       (v + (w >> 3)) * 128 + (w & 7) * 16) = make_uint4(0, 0, 0, 0);
-                                        }
-                                        md::fence_async_shared();
-                                        if (rank == 1) asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                                        __syncwarp();
-                                    }
-                                    // the second CTA's word to the first: loaded and cleared.  Relaxed: a
-                                    // release at each stage took longer than the stage's products, and
-                                    // only cleared stages have writes of this warp to order.
-                                    if (rank == 1 && lane == 0)
-                                        md::mbar_arrive_cluster_relaxed(md::map_rank(md::smem_addr(&b->full[at.s]), 0));
+                                if (!(ok = await(&b->full[at.s], at.parity))) break;
+                                const int v = q.count - (from + i + j) * kTileK;  // weight gradient: rows left
+                                if (kWg && v < kTileK) {
+                                    steps[j] = (v + 15) / 16;
+                                    clear(at.s, v, steps[j], (q.n / 2 + 63) / 64, subs);
+                                    if (!(ok = await(&b->cleared[at.s], tails >> at.s & 1u))) break;
+                                    tails ^= 1u << at.s;
                                 }
                                 md::tmem_fence_after();
                                 at.next();
-                                if (!kWg || rank == 0) ok = product(0, i + j, s[j], steps[j]);
+                                ok = product(0, i + j, s[j], steps[j]);
                             }
-                            if (!kWg || rank == 0)
-                                for (int j = 0; ok && subs == 2 && j < g; ++j) ok = product(1, i + j, s[j], steps[j]);
+                            for (int j = 0; ok && subs == 2 && j < g; ++j) ok = product(1, i + j, s[j], steps[j]);
                         }
                     }
                 }
-                if (rank == 0 && lane == 0) {  // await the MMAs in flight, whoever gave up
-                    md::mma_commit<2>(&b->drain);
-                    md::mbar_wait_bounded(&b->drain, 0, kDrainPolls);
-                }
+                md::mma_commit<2>(&b->drain);  // await the MMAs in flight, whoever gave up
+                md::mbar_wait_bounded(&b->drain, 0, kDrainPolls);
             }
         }
     } else {

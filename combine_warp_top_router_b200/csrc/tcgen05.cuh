@@ -78,6 +78,19 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// whether phase `parity` of `bar` is complete, without waiting
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0u;
+}
+
 // without ordering this thread's earlier accesses
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t addr)
 {
@@ -97,19 +110,38 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *m)
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 
+// The copies, products and their barrier words below are issued by one elected
+// lane (always the same) of a converged warp: the operands then stay in uniform
+// registers, where a branch around them for lane 0 cost some 200 cycles a product.
+
+__device__ __forceinline__ void expect_tx_one(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(smem_addr(bar)),
+        "r"(bytes)
+        : "memory");
+}
+
 // One box of a 2- or 3-dimensional map into this CTA's shared memory; `bar` is
-// a shared::cluster address (CG == 2: the leader CTA's barrier).
+// a shared::cluster address (CG == 2: of either CTA of the pair).
 template <int CG>
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, int c0, int c1, uint32_t bar)
 {
     if (CG == 1)
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                     " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(m), "r"(c0), "r"(c1), "r"(bar)
-                     : "memory");
+        asm volatile(
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+            " @e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(dst),
+            "l"(m), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
     else
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-                     " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(m), "r"(c0), "r"(c1), "r"(bar)
-                     : "memory");
+        asm volatile(
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+            " @e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(dst),
+            "l"(m), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
 }
 
 template <int CG>
@@ -117,13 +149,19 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
                                             uint32_t bar)
 {
     if (CG == 1)
-        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                     " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-                     : "memory");
+        asm volatile(
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+            " @e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
+            "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+            : "memory");
     else
-        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-                     " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-                     : "memory");
+        asm volatile(
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+            " @e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
+            "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+            : "memory");
 }
 
 // generic-proxy writes to shared memory become visible to the async proxy
@@ -200,37 +238,39 @@ __device__ __forceinline__ uint32_t mma_desc(int m, int n, bool a_mn, bool b_mn)
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// D[tmem] (+)= A B, K = 16; one thread (CG == 2: of the leader CTA)
+// D[tmem] (+)= A B, K = 16 (CG == 2: by the leader CTA)
 template <int CG>
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
 {
     const uint32_t acc = accumulate ? 1u : 0u;
     if (CG == 1)
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+            "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.u32 p, %4, 0;\n"
+            " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
             "l"(a), "l"(b), "r"(idesc), "r"(acc)
             : "memory");
     else
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+            "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.u32 p, %4, 0;\n"
+            " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
             "l"(a), "l"(b), "r"(idesc), "r"(acc)
             : "memory");
 }
 
-// this thread's MMAs so far arrive on `bar` when done (CG == 2: on the barrier
-// at the same place in both CTAs)
+// the elected lane's MMAs so far arrive on `bar` when done (CG == 2: on the
+// barrier at the same place in both CTAs)
 template <int CG>
 __device__ __forceinline__ void mma_commit(uint64_t *bar)
 {
     if (CG == 1)
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                         smem_addr(bar))
-                     : "memory");
+        asm volatile(
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+            " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_addr(bar))
+            : "memory");
     else
         asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+            " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(
                 smem_addr(bar)),
             "h"((uint16_t)3)
             : "memory");

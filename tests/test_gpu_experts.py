@@ -206,6 +206,22 @@ def test_wgrad_of_long_experts(counts):
     assert torch.equal(md.md_expert_wgrad(dy, x, off, cnt, out_dtype=torch.bfloat16), want.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("hi", [1, 16, 63, 64, 130])
+def test_wgrad_of_many_short_experts(hi):
+    """Tiles of one to three blocks, so that the loads run several tiles ahead."""
+    E, N, K = 96, 1032, 264
+    counts = np.random.default_rng(hi).integers(1, hi + 1, E).tolist()
+    off, cnt, rows, spans = groups(counts, seed=hi, gap=1)
+    dy, x = ints(1, rows, N, hi=2), ints(2, rows, K, hi=2)
+    mine = owned(rows, spans)
+    dy[~mine], x[~mine] = float("nan"), float("nan")
+    st = md.new_status(DEV)
+    dw = md.md_expert_wgrad(dy, x, off, cnt, dev_status=st)
+    md.check_status(st)
+    for e, o, c in spans:
+        assert torch.equal(dw[e].double(), dy[o:o + c].double().t() @ x[o:o + c].double())
+
+
 @pytest.mark.parametrize("op", ["nk", "kn", "gated", "wgrad"])
 def test_many_tiles_of_two_products(op):
     """Enough tiles that each takes 512 weight rows, some of whose second halves are partly or
