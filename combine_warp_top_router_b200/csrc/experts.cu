@@ -134,9 +134,13 @@ __device__ __forceinline__ void drain_loads(Turn at, int used, uint64_t *full)
 // Experts' starts and counts, the running number of row tiles, and the
 // experts in the order of their tiles; in shared memory.
 struct Table {
-    int *off, *cnt, *pre, *order;
-    __device__ __forceinline__ Table(void *at, int E)
-        : off(static_cast<int *>(at)), cnt(off + E), pre(cnt + E), order(pre + E) {}
+    int *base;
+    int E;
+    __device__ __forceinline__ Table(void *at, int n) : base(static_cast<int *>(at)), E(n) {}
+    __device__ __forceinline__ int &off(int e) const { return base[e]; }
+    __device__ __forceinline__ int &cnt(int e) const { return base[E + e]; }
+    __device__ __forceinline__ int &pre(int i) const { return base[2 * E + i]; }
+    __device__ __forceinline__ int &order(int i) const { return base[3 * E + i]; }
     static size_t bytes(int E) { return 16 * (size_t)E; }
 };
 
@@ -149,9 +153,9 @@ __device__ __forceinline__ void read_ranges(const Table &tab, const Args &a)
             md::report(a.status, MD_ERR_DATA);
             c = 0;
         }
-        tab.off[e] = c > 0 ? o : 0;
-        tab.cnt[e] = c;
-        tab.order[e] = e;
+        tab.off(e) = c > 0 ? o : 0;
+        tab.cnt(e) = c;
+        tab.order(e) = e;
     }
 }
 
@@ -172,13 +176,13 @@ template <int MODE>
 __device__ __forceinline__ void sort_experts(const Table &tab, const Args &a)
 {
     for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-        tab.pre[e] = MODE == kWgrad ? tab.cnt[e] : tile_rows<2, 256>(tab.cnt[e]);
+        tab.pre(e) = MODE == kWgrad ? tab.cnt(e) : tile_rows<2, 256>(tab.cnt(e));
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-        const int c = tab.pre[e];
+        const int c = tab.pre(e);
         int before = 0;
-        for (int o = 0; o < a.E; ++o) before += tab.pre[o] > c || (tab.pre[o] == c && o < e);
-        tab.order[before] = e;
+        for (int o = 0; o < a.E; ++o) before += tab.pre(o) > c || (tab.pre(o) == c && o < e);
+        tab.order(before) = e;
     }
     __syncthreads();
 }
@@ -191,14 +195,14 @@ __device__ __forceinline__ void count_tiles(const Table &tab, Shared *sh, const 
     int run = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
         const int e = e0 + lane;
-        const int own = e < a.E ? (tab.cnt[tab.order[e]] + BN - 1) / BN : 0;
+        const int own = e < a.E ? (tab.cnt(tab.order(e)) + BN - 1) / BN : 0;
         int v = own;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, v, d);
             if (lane >= d) v += o;
         }
-        if (e < a.E) tab.pre[e] = run + v - own;
+        if (e < a.E) tab.pre(e) = run + v - own;
         run += __shfl_sync(0xffffffffu, v, 31);
     }
     if (lane == 0) sh->tiles = run;
@@ -212,14 +216,14 @@ __device__ __forceinline__ Tile rows_at(int rt, const Table &tab, const Args &a)
     int lo = 0, hi = a.E;  // last place in the order whose first tile is at or before rt
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (tab.pre[mid] <= rt) lo = mid;
+        if (tab.pre(mid) <= rt) lo = mid;
         else hi = mid;
     }
     Tile q;
-    q.e = tab.order[lo];
-    const int c = tab.cnt[q.e], each = tile_rows<CG, BN>(c), at = (rt - tab.pre[lo]) * each;
+    q.e = tab.order(lo);
+    const int c = tab.cnt(q.e), each = tile_rows<CG, BN>(c), at = (rt - tab.pre(lo)) * each;
     q.m0 = 0;
-    q.r0 = (int64_t)tab.off[q.e] + at;
+    q.r0 = (int64_t)tab.off(q.e) + at;
     q.count = c - at < each ? c - at : each;
     q.c0 = 0;
     q.n = (q.count + kGran - 1) / kGran * kGran;
@@ -386,8 +390,8 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
     __shared__ __align__(16) FewBars bars;
     Shared *sh = &shared;
     FewBars *b = &bars;
-    unsigned char *base = reinterpret_cast<unsigned char *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    // an offset, not a rounded address: the compiler then knows shared memory as such
+    unsigned char *base = smem_raw + (-md::smem_addr(smem_raw) & 1023u);
     unsigned char *staging = base + P::kStages * P::kStageBytes;
     const Table tab(staging + kStagingBytes, a.E);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -616,68 +620,58 @@ __device__ __forceinline__ int blocks_at(int i, int kb, int subs)
     return subs == 2 && kb - i >= 2 && (i == 0 || i == kb - 2) ? 2 : 1;
 }
 
-// 32 columns from column c on of dw's rows row0 .. row0 + 31, one row in each lane of
-// the warp, turned around in the warp's 2 KB of staging (swizzled: no bank is hit
-// twice) so that global accesses are whole 128-byte lines (bf16: halves).
-// Straight from registers, a row to a lane, each store touched 32 lines and
-// the stores took as long as 2048 rows' products.
+// 64 bytes of columns of dw's rows row0 .. row0 + 31, one row in each lane of the warp,
+// turned around in the warp's 2 KB of staging (swizzled: no bank is hit twice), so that
+// a store touches 8 rows and not 32.  (Straight from registers, the stores took
+// as long as 2048 rows' products.)  `to` is the first row's place, `bytes`
+// what is left of a row there, `pitch` a row of dw, in bytes.
+__device__ __forceinline__ void put_64(const uint32_t (&w)[16], char *to, int rows, int bytes, uint32_t pitch, bool add,
+                                       unsigned char *st)
+{
+    const int lane = threadIdx.x & 31, p = (lane & 3) * 16, r0 = lane >> 2;
+    const int sw = (lane >> 1 & 3) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4 *>(st + lane * 64 + (i * 16 ^ sw)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    __syncwarp();
+    const int live = p < bytes ? rows : 0;
+    float4 f[4], o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = j * 8 + r0;
+        f[j] = *reinterpret_cast<const float4 *>(st + r * 64 + (p ^ (r >> 1 & 3) * 16));
+        o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (add && r < live) o[j] = *reinterpret_cast<const float4 *>(to + r * pitch + p);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = j * 8 + r0;
+        if (add) f[j] = make_float4(o[j].x + f[j].x, o[j].y + f[j].y, o[j].z + f[j].z, o[j].w + f[j].w);
+        if (r < live) *reinterpret_cast<float4 *>(to + r * pitch + p) = f[j];
+    }
+}
+
+// 32 columns from column c on of dw's rows from row0 on.
 __device__ __forceinline__ void put_rows(const uint32_t (&v)[32], const Args &a, int e, int row0, int c, bool add,
                                          unsigned char *st)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t first = ((int64_t)e * a.n + row0) * a.k + c;  // rows below it: 32-bit offsets
+    const int64_t first = ((int64_t)e * a.n + row0) * a.k + c;
+    const int rows = a.n - row0, left = a.k - c;
+    uint32_t w[16];
     if (a.out_bf16) {
-        const int sw = (lane >> 1 & 3) * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-                w[h] = md::pack_bf16x2(__uint_as_float(v[8 * i + 2 * h]), __uint_as_float(v[8 * i + 2 * h + 1]));
-            *reinterpret_cast<uint4 *>(st + lane * 64 + (i * 16 ^ sw)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        __syncwarp();
-        const int p = lane & 3;
-        if (c + p * 8 < a.k) {
-            __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.y) + first + p * 8;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = j * 8 + (lane >> 2);
-                if (row0 + r < a.n)
-                    *reinterpret_cast<uint4 *>(to + r * a.k) =
-                        *reinterpret_cast<const uint4 *>(st + r * 64 + (p * 16 ^ (r >> 1 & 3) * 16));
-            }
-        }
-        __syncwarp();
+        for (int i = 0; i < 16; ++i)
+            w[i] = md::pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        put_64(w, static_cast<char *>(a.y) + first * 2, rows, left * 2, (uint32_t)a.k * 2, false, st);
         return;
     }
-    const int p = lane & 7, sw = p * 16;
-    float *to = static_cast<float *>(a.y) + first + p * 4;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // 16 rows at a time
-        if (lane >> 4 == h) {
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4 *>(st + (lane & 15) * 128 + (i * 16 ^ sw)) =
-                    make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        }
-        __syncwarp();
-        if (c + p * 4 < a.k) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = j * 4 + (lane >> 3);
-                if (row0 + h * 16 + r < a.n) {
-                    float4 f = *reinterpret_cast<const float4 *>(st + r * 128 + (sw ^ (r & 7) * 16));
-                    float4 *at = reinterpret_cast<float4 *>(to + (h * 16 + r) * a.k);
-                    if (add) {
-                        const float4 o = *at;
-                        f = make_float4(o.x + f.x, o.y + f.y, o.z + f.z, o.w + f.w);
-                    }
-                    *at = f;
-                }
-            }
-        }
-        __syncwarp();
+        for (int i = 0; i < 16; ++i) w[i] = v[16 * h + i];
+        put_64(w, static_cast<char *>(a.y) + first * 4 + 64 * h, rows, (left - 16 * h) * 4, (uint32_t)a.k * 4, add, st);
     }
 }
 
@@ -694,8 +688,8 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
     __shared__ __align__(16) WideBars bars;
     Shared *sh = &shared;
     WideBars *b = &bars;
-    unsigned char *base = reinterpret_cast<unsigned char *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    // an offset, not a rounded address: the compiler then knows shared memory as such
+    unsigned char *base = smem_raw + (-md::smem_addr(smem_raw) & 1023u);
     unsigned char *staging = base + W::kParts * W::kPart;
     const Table tab(staging + kStagingBytes, a.E);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -741,9 +735,9 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
         Tile q;
         if (kWg) {
             const int per = mt * ct, at = t / per, i = t - at * per, ci = i / mt;
-            q.e = tab.order[at];
-            q.r0 = tab.off[q.e];
-            q.count = tab.cnt[q.e];
+            q.e = tab.order(at);
+            q.r0 = tab.off(q.e);
+            q.count = tab.cnt(q.e);
             q.c0 = ci * BN;
             q.n = (min(a.k - q.c0, BN) + 31) / 32 * 32;
         } else {
@@ -875,8 +869,8 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                     const uint32_t idesc = md::mma_desc(256, q.n, !kAKMajor, kWg);
                     for (int from = 0, kb; ok && from < blocks; from += kb, opened += subs) {
                         kb = min(blocks - from, segment);
-                        // block i of one sub, in stage s, the first `steps` sixteenths of it
-                        auto product = [&](int sub, int i, int s, int steps) {
+                        // block i of one sub, in stage s; of a last block as many sixteenths as hold rows
+                        auto product = [&](int sub, int i, int s) {
                             const uint32_t acc = opened + sub;
                             if (i == 0) {
                                 if (!await(&b->tempty[acc & 1], ((acc >> 1) & 1u) ^ 1u)) return false;
@@ -884,13 +878,14 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                             }
                             const uint32_t off = (uint32_t)(s * stage_bytes) >> 4;
                             const uint64_t da = da0 + off + (sub ? 2 * W::kPart >> 4 : 0), db = db0 + off + (W::kPart >> 4);
-                            if (!kWg || steps == kTileK / 16) {
+                            const int v = q.count - (from + i) * kTileK;
+                            if (!kWg || v > kTileK - 16) {
 #pragma unroll
                                 for (int j = 0; j < kTileK / 16; ++j)
                                     md::mma_bf16<2>(tmem + (acc & 1) * BN, da + j * kAStep, db + j * kBStep, idesc, i > 0 || j > 0);
                             } else {
 #pragma unroll 1
-                                for (int j = 0; j < steps; ++j)
+                                for (int j = 0; j * 16 < v; ++j)
                                     md::mma_bf16<2>(tmem + (acc & 1) * BN, da + j * kAStep, db + j * kBStep, idesc, i > 0 || j > 0);
                             }
                             if (sub == subs - 1) md::mma_commit<2>(&b->empty[s]);
@@ -899,23 +894,22 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                         };
                         for (int i = 0, g; ok && i < kb; i += g) {
                             g = blocks_at(i, kb, subs);
-                            int s[2], steps[2];
+                            const int s0 = at.s;
                             for (int j = 0; ok && j < g; ++j) {
-                                s[j] = at.s;
-                                steps[j] = kTileK / 16;
                                 if (!(ok = await(&b->full[at.s], at.parity))) break;
                                 const int v = q.count - (from + i + j) * kTileK;  // weight gradient: rows left
                                 if (kWg && v < kTileK) {
-                                    steps[j] = (v + 15) / 16;
-                                    clear(at.s, v, steps[j], (q.n / 2 + 63) / 64, subs);
+                                    clear(at.s, v, (v + 15) / 16, (q.n / 2 + 63) / 64, subs);
                                     if (!(ok = await(&b->cleared[at.s], tails >> at.s & 1u))) break;
                                     tails ^= 1u << at.s;
                                 }
                                 md::tmem_fence_after();
+                                ok = product(0, i + j, at.s);
                                 at.next();
-                                ok = product(0, i + j, s[j], steps[j]);
                             }
-                            for (int j = 0; ok && subs == 2 && j < g; ++j) ok = product(1, i + j, s[j], steps[j]);
+                            if (subs == 2)
+                                for (int j = 0, st = s0; ok && j < g; ++j, st = st + 1 == stages ? 0 : st + 1)
+                                    ok = product(1, i + j, st);
                         }
                     }
                 }
@@ -949,27 +943,27 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
             if (lane == 0) md::mbar_arrive_cluster_relaxed(md::map_rank(md::smem_addr(&b->tempty[acc & 1]), 0));
             ++acc;
         };
-        constexpr bool kThree = kWg || MODE == kGated;  // their put needs more registers
-        // the subs' accumulators, out through put(values, sub, run).  Sub 1's is taken when half of
-        // sub 0's registers are free again.
+        // the subs' accumulators, out through put(values, sub, run).  Sub 1's is taken as soon as
+        // put's own registers allow: a spilled value would come back from L2, under all that
+        // traffic some 1500 cycles a load.
+        constexpr int kBefore = kWg ? 4 : MODE == kGated ? 3 : 2;
         auto results = [&](int subs, auto put) __attribute__((always_inline)) {
             uint32_t v[4][32];
             take(v);
             if (!ok) return;
-            put(v[0], 0, 0);
-            put(v[1], 0, 1);
-            if (kThree) put(v[2], 0, 2);
+#pragma unroll
+            for (int i = 0; i < kBefore; ++i) put(v[i], 0, i);
             if (subs == 2) {
                 uint32_t w[4][32];
                 take(w);
                 if (!ok) return;
-                if (!kThree) put(v[2], 0, 2);
-                put(v[3], 0, 3);
+#pragma unroll
+                for (int i = kBefore; i < 4; ++i) put(v[i], 0, i);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) put(w[i], 1, i);
             } else {
-                if (!kThree) put(v[2], 0, 2);
-                put(v[3], 0, 3);
+#pragma unroll
+                for (int i = kBefore; i < 4; ++i) put(v[i], 0, i);
             }
         };
         for (int round = 0; ok && round < rounds; ++round) {
