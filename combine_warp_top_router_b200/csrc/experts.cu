@@ -39,6 +39,23 @@ constexpr int kMaxSplit = 4; // CTAs that share a contraction (few rows)
 constexpr long long kPolls = 1ll << 22;
 constexpr long long kDrainPolls = 1ll << 20;
 
+// Division by a number fixed at launch: exact for 0 <= x < 2^31 (d >= 1), by the
+// round-up reciprocal of Granlund and Montgomery, with x below 2^31 in 33 bits.
+struct FastDiv {
+    uint32_t d, mul, shift;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t by) : d(by), mul(0), shift(0)
+    {
+        while (((uint64_t)1 << shift) < d) ++shift;  // ceil(log2 d)
+        // mul = ceil(2^(31 + shift) / d) <= 2^32 - 1 for d >= 2; x mul < 2^63
+        mul = d == 1 ? 0 : (uint32_t)((((uint64_t)1 << (31 + shift)) + d - 1) / d);
+    }
+    __host__ __device__ __forceinline__ int div(int x) const
+    {
+        return d == 1 ? x : (int)(((uint64_t)(uint32_t)x * mul) >> (31 + shift));
+    }
+};
+
 struct Args {
     const int32_t *offsets, *counts;
     int64_t rows;
@@ -50,6 +67,8 @@ struct Args {
     uint8_t *codes, *scales;  // gated: checkpoint or NULL
     int out_bf16, accumulate; // wgrad
     int subs;     // k_expert_wide: M = 256 products to a tile, at most
+    FastDiv mt;   // tiles along the weight rows
+    FastDiv per;  // wgrad: tiles of an expert
     int split;    // k_expert_few: CTAs (a cluster) that share each tile's contraction; each cluster has one tile
     int32_t *status;
     long long polls;
@@ -98,6 +117,7 @@ struct Tile {
     int count;       // rows (wgrad: of the expert)
     int c0;          // wgrad: first dw column
     int n;           // MMA N
+    int subs;        // k_expert_wide: M = 256 products
 };
 
 // A place in the ring of stages: the stage and the parity of its turn.
@@ -394,7 +414,7 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
     unsigned char *base = smem_raw + (-md::smem_addr(smem_raw) & 1023u);
     unsigned char *staging = base + P::kStages * P::kStageBytes;
     const Table tab(staging + kStagingBytes, a.E);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int share = a.split > 1 ? (int)md::cluster_rank() : 0;  // of the contraction
 
     if (threadIdx.x == 0) {
@@ -423,16 +443,16 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
     md::tmem_fence_after();
     const uint32_t tmem = sh->tmem;
 
-    const int mt = (a.n + P::kWidth - 1) / P::kWidth;  // tiles along the weight rows
-    const int total = sh->tiles * mt;                  // the host keeps it below 2^30
+    const int total = sh->tiles * (int)a.mt.d;  // the host keeps it below 2^30
     const int first = blockIdx.x / a.split, step = gridDim.x / a.split;
     const uint32_t sbase = md::smem_addr(base);
     // blocks of the contraction: [kb0, kb1) in this CTA
     const int kblocks = (a.k + kTileK - 1) / kTileK;
     const int kb0 = kblocks * share / a.split, kb1 = kblocks * (share + 1) / a.split;
     auto tile_of = [&](int t) {
-        Tile q = rows_at<1, BN>(t / mt, tab, a);
-        q.m0 = t % mt * P::kWidth;
+        const int rt = a.mt.div(t);
+        Tile q = rows_at<1, BN>(rt, tab, a);
+        q.m0 = (t - rt * (int)a.mt.d) * P::kWidth;
         return q;
     };
 
@@ -620,65 +640,47 @@ __device__ __forceinline__ int blocks_at(int i, int kb, int subs)
     return subs == 2 && kb - i >= 2 && (i == 0 || i == kb - 2) ? 2 : 1;
 }
 
-// 64 bytes of columns of dw's rows row0 .. row0 + 31, one row in each lane of the warp,
-// turned around in the warp's 2 KB of staging (swizzled: no bank is hit twice), so that
-// a store touches 8 rows and not 32.  (Straight from registers, the stores took
-// as long as 2048 rows' products.)  `to` is the first row's place, `bytes`
-// what is left of a row there, `pitch` a row of dw, in bytes.
-__device__ __forceinline__ void put_64(const uint32_t (&w)[16], char *to, int rows, int bytes, uint32_t pitch, bool add,
-                                       unsigned char *st)
+// 32 columns of dw's rows, one row in each lane of the warp, through the warp's 2 KB of
+// staging in boxes of 32 rows by 64 bytes, stored (or added) by TMA: its engine does not
+// hold up the warp, which has the next accumulator to empty, and the map cuts the
+// box at dw's edges.  Stores straight from registers touch 32 lines each; they
+// reached 4.2 TB/s and held sub 1's accumulator for 8000 cycles.
+__device__ __forceinline__ void put_rows(const uint32_t (&v)[32], const CUtensorMap *map, const Args &a, int c, int row0,
+                                         int e, bool add, unsigned char *st)
 {
-    const int lane = threadIdx.x & 31, p = (lane & 3) * 16, r0 = lane >> 2;
-    const int sw = (lane >> 1 & 3) * 16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4 *>(st + lane * 64 + (i * 16 ^ sw)) =
-            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    __syncwarp();
-    const int live = p < bytes ? rows : 0;
-    float4 f[4], o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int r = j * 8 + r0;
-        f[j] = *reinterpret_cast<const float4 *>(st + r * 64 + (p ^ (r >> 1 & 3) * 16));
-        o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (add && r < live) o[j] = *reinterpret_cast<const float4 *>(to + r * pitch + p);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int r = j * 8 + r0;
-        if (add) f[j] = make_float4(o[j].x + f[j].x, o[j].y + f[j].y, o[j].z + f[j].z, o[j].w + f[j].w);
-        if (r < live) *reinterpret_cast<float4 *>(to + r * pitch + p) = f[j];
-    }
-}
-
-// 32 columns from column c on of dw's rows from row0 on.
-__device__ __forceinline__ void put_rows(const uint32_t (&v)[32], const Args &a, int e, int row0, int c, bool add,
-                                         unsigned char *st)
-{
-    const int64_t first = ((int64_t)e * a.n + row0) * a.k + c;
-    const int rows = a.n - row0, left = a.k - c;
-    uint32_t w[16];
-    if (a.out_bf16) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            w[i] = md::pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-        put_64(w, static_cast<char *>(a.y) + first * 2, rows, left * 2, (uint32_t)a.k * 2, false, st);
-        return;
-    }
+    const int lane = threadIdx.x & 31, sw = (lane >> 1 & 3) * 16;  // the map's 64-byte swizzle
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+        uint32_t w[16];
+        if (a.out_bf16) {
+            if (h == 1) break;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = v[16 * h + i];
-        put_64(w, static_cast<char *>(a.y) + first * 4 + 64 * h, rows, (left - 16 * h) * 4, (uint32_t)a.k * 4, add, st);
+            for (int i = 0; i < 16; ++i) w[i] = md::pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        } else {
+            if (c + 16 * h >= a.k) break;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = v[16 * h + i];
+        }
+        md::bulk_wait_read<0>();  // lane 0's store that read the buffer; the others have none
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4 *>(st + lane * 64 + (i * 16 ^ sw)) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        md::fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            if (add) md::tma_add_3d(map, md::smem_addr(st), c + 16 * h, row0, e);
+            else md::tma_store_3d(map, md::smem_addr(st), c + 16 * h, row0, e);
+            md::bulk_commit();
+        }
     }
 }
 
 template <int MODE>
 __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
     k_expert_wide(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                  const __grid_constant__ Args a)
+                  const __grid_constant__ CUtensorMap map_d, const __grid_constant__ Args a)
 {
     using W = Wide<MODE>;
     constexpr int BN = 256;
@@ -692,7 +694,7 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
     unsigned char *base = smem_raw + (-md::smem_addr(smem_raw) & 1023u);
     unsigned char *staging = base + W::kParts * W::kPart;
     const Table tab(staging + kStagingBytes, a.E);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = (int)md::cluster_rank();
 
     if (threadIdx.x == 0) {
@@ -724,8 +726,8 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
     const uint32_t tmem = sh->tmem;
 
     const int width = a.subs * W::kSub;  // output columns (weight gradient: rows of dw) of a tile
-    const int mt = (a.n + width - 1) / width, ct = (a.k + BN - 1) / BN;
-    const int total = kWg ? a.E * mt * ct : sh->tiles * mt;  // the host keeps it below 2^30
+    const int mt = (int)a.mt.d;
+    const int total = kWg ? a.E * (int)a.per.d : sh->tiles * mt;  // the host keeps it below 2^30
     const int step = gridDim.x / 2, place = blockIdx.x / 2, rounds = (total + step - 1) / step;
     // the cluster's tile of a round, dealt back and forth; `total` or more: none
     auto deal = [&](int round) { return round * step + (round & 1 ? step - 1 - place : place); };
@@ -733,21 +735,25 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
     const int stages = W::kParts / (a.subs + 1), stage_bytes = (a.subs + 1) * W::kPart;
     auto tile_of = [&](int t) {
         Tile q;
+        int mi;  // tile along the weight rows
         if (kWg) {
-            const int per = mt * ct, at = t / per, i = t - at * per, ci = i / mt;
+            const int at = a.per.div(t), i = t - at * (int)a.per.d, ci = a.mt.div(i);
+            mi = i - ci * mt;
             q.e = tab.order(at);
             q.r0 = tab.off(q.e);
             q.count = tab.cnt(q.e);
             q.c0 = ci * BN;
             q.n = (min(a.k - q.c0, BN) + 31) / 32 * 32;
         } else {
-            q = rows_at<2, BN>(t / mt, tab, a);
+            const int rt = a.mt.div(t);
+            mi = t - rt * mt;
+            q = rows_at<2, BN>(rt, tab, a);
         }
-        q.m0 = t % mt * width + rank * (W::kSub / 2);
+        q.m0 = mi * width + rank * (W::kSub / 2);
+        // the last tile along the weight rows may have one sub where others have two
+        q.subs = a.subs == 2 && mi * width + W::kSub < a.n ? 2 : 1;
         return q;
     };
-    // the last tile along the weight rows may have one sub where others have two
-    auto subs_of = [&](int t) { return a.subs == 2 && t % mt * width + W::kSub < a.n ? 2 : 1; };
     // blocks of the tile's contraction
     auto blocks_of = [&](const Tile &q) { return ((kWg ? q.count : a.k) + kTileK - 1) / kTileK; };
     // blocks that one accumulator sums
@@ -766,7 +772,7 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                     const int t = deal(round);
                     if (t >= total) continue;
                     const Tile q = tile_of(t);
-                    const int subs = subs_of(t), kb = blocks_of(q);
+                    const int subs = q.subs, kb = blocks_of(q);
                     const int half = q.n / 2, boxes = (half + 63) / 64;  // N-side lines of this CTA
                     const int r0 = (int)q.r0 + (kWg ? 0 : rank * half), c0 = q.c0 + rank * half;
                     const uint32_t bytes = warp == kLoadWarp ? subs * W::kPart : boxes * 8192;
@@ -848,7 +854,7 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                     at.back();
                     if (!warp_wait(&b->tail[at.s], tails >> at.s & 1u, sh, a)) break;
                     tails ^= 1u << at.s;
-                    clear(at.s, v, (v + 15) / 16, (q.n / 2 + 63) / 64, subs_of(t));
+                    clear(at.s, v, (v + 15) / 16, (q.n / 2 + 63) / 64, q.subs);
                     if (lane == 0) md::mbar_arrive_cluster(md::map_rank(md::smem_addr(&b->cleared[at.s]), 0));
                     at.next();
                 }
@@ -865,7 +871,7 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                     const int t = deal(round);
                     if (t >= total) continue;
                     const Tile q = tile_of(t);
-                    const int subs = subs_of(t), blocks = blocks_of(q);
+                    const int subs = q.subs, blocks = blocks_of(q);
                     const uint32_t idesc = md::mma_desc(256, q.n, !kAKMajor, kWg);
                     for (int from = 0, kb; ok && from < blocks; from += kb, opened += subs) {
                         kb = min(blocks - from, segment);
@@ -929,7 +935,12 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
         bool ok = true;
         // this warp's columns of an accumulator, in four runs of 32, into registers (all of them,
         // the tile's or not: a register that is loaded on a condition stays taken throughout)
-        auto take = [&](uint32_t (&v)[4][32]) __attribute__((always_inline)) {
+        auto take = [&](uint32_t (&v)[4][32], bool empty) __attribute__((always_inline)) {
+            if (kWg && empty) {  // an expert without rows
+#pragma unroll
+                for (int i = 0; i < 128; ++i) v[i >> 5][i & 31] = 0;
+                return;
+            }
             ok = epilogue_wait(&b->tfull[acc & 1], (acc >> 1) & 1u, sh, a);
             if (!ok) return;
             md::tmem_fence_after();
@@ -946,16 +957,16 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
         // the subs' accumulators, out through put(values, sub, run).  Sub 1's is taken as soon as
         // put's own registers allow: a spilled value would come back from L2, under all that
         // traffic some 1500 cycles a load.
-        constexpr int kBefore = kWg ? 4 : MODE == kGated ? 3 : 2;
+        constexpr int kBefore = MODE == kGated ? 3 : 2;
         auto results = [&](int subs, auto put) __attribute__((always_inline)) {
             uint32_t v[4][32];
-            take(v);
+            take(v, false);
             if (!ok) return;
 #pragma unroll
             for (int i = 0; i < kBefore; ++i) put(v[i], 0, i);
             if (subs == 2) {
                 uint32_t w[4][32];
-                take(w);
+                take(w, false);
                 if (!ok) return;
 #pragma unroll
                 for (int i = kBefore; i < 4; ++i) put(v[i], 0, i);
@@ -970,23 +981,25 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
             const int t = deal(round);
             if (t >= total) continue;
             const Tile q = tile_of(t);
-            const int subs = subs_of(t);
+            const int subs = q.subs;
             if (kWg) {
                 const int blocks = blocks_of(q), cols = min(a.k - q.c0, BN);
                 if (blocks == 0 && a.accumulate) continue;
-                for (int from = 0; from == 0 || (ok && from < blocks); from += min(segment, max(blocks - from, 1))) {
+                for (int from = 0; from == 0 || (ok && from < blocks); from += min(segment, max(blocks - from, 1))) {  // once if empty
                     const bool add = a.accumulate || from > 0;
+                    if (from > 0) md::bulk_wait_all();  // what this adds to is written
                     auto put = [&](const uint32_t (&x)[32], int sub, int i) __attribute__((always_inline)) {
                         const int c = group * 128 + i * 32, row0 = q.m0 + sub * W::kSub + (warp & 3) * 32;
-                        if (c < cols && row0 < a.n) put_rows(x, a, q.e, row0, q.c0 + c, add, staging + warp * 2048);
+                        if (c < cols && row0 < a.n) put_rows(x, &map_d, a, q.c0 + c, row0, q.e, add, staging + warp * 2048);
                     };
-                    if (blocks == 0) {
-                        uint32_t none[32] = {};
-                        for (int sub = 0; sub < subs; ++sub)
-                            for (int i = 0; i < 4; ++i) put(none, sub, i);
-                        break;
+#pragma unroll 1
+                    for (int sub = 0; ok && sub < subs; ++sub) {
+                        uint32_t v[4][32];
+                        take(v, blocks == 0);
+                        if (!ok) break;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) put(v[i], sub, i);
                     }
-                    results(subs, put);
                 }
             } else {
                 auto put = [&](const uint32_t (&x)[32], int sub, int i) __attribute__((always_inline)) {
@@ -999,6 +1012,7 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
         }
     }
 
+    if (kWg) md::bulk_wait_all();
     // ---- end: nobody leaves while its pair may still read its shared memory
     __syncwarp();
     md::tmem_fence_before();
@@ -1011,9 +1025,9 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
 // ------------------------------------------------------------------ host
 
 // One launch in clusters of `members` CTAs.
-template <class Kernel>
+template <class Kernel, class... Params>
 int launch(Kernel kernel, int threads, size_t smem, size_t most_smem, std::atomic<uint64_t> &setup, int64_t clusters,
-           int members, const CUtensorMap &ma, const CUtensorMap &mb, const Args &a, cudaStream_t s)
+           int members, cudaStream_t s, const Params &...params)
 {
     md::once_per_device(setup, [&] {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem) != cudaSuccess)
@@ -1032,7 +1046,7 @@ int launch(Kernel kernel, int threads, size_t smem, size_t most_smem, std::atomi
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, ma, mb, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernel, params...) != cudaSuccess) {
         cudaGetLastError();
         return MD_ERR_CUDA;
     }
@@ -1066,6 +1080,7 @@ int run_few(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int
         !md::make_map(&mb, x, kBf16, 2, a.k, rows, 0, 64, P::kBox))
         return MD_ERR_CUDA;
     const int mt = (a.n + P::kWidth - 1) / P::kWidth;
+    a.mt = FastDiv((uint32_t)mt);
     const int64_t tiles = (rows / P::BN + (rows < a.E ? rows : a.E)) * mt;  // at most
     if (tiles > kMostTiles) return MD_ERR_UNSUPPORTED;
     // Few tiles leave SMs idle and each tile streams its weights through one SM: clusters of
@@ -1075,8 +1090,8 @@ int run_few(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int
     while (a.split < kMaxSplit && tiles * a.split * 2 <= md::sm_count() && a.k >= a.split * 2 * 4 * kTileK)
         a.split *= 2;
     static std::atomic<uint64_t> setup{0};
-    return launch(k_expert_few<MODE>, P::kThreads, P::smem(a.E), P::smem(MD_MAX_EXPERTS), setup, tiles, a.split, ma, mb,
-                  a, s);
+    return launch(k_expert_few<MODE>, P::kThreads, P::smem(a.E), P::smem(MD_MAX_EXPERTS), setup, tiles, a.split, s, ma,
+                  mb, a);
 }
 
 // Two subs to a tile where that still gives every pair of SMs several tiles.
@@ -1093,10 +1108,11 @@ int run_wide(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, in
     const int64_t row_tiles = rows / 256 + (rows < a.E ? rows : a.E);  // at most
     a.subs = subs_for(row_tiles * ((a.n + W::kSub - 1) / W::kSub));
     const int mt = (a.n + a.subs * W::kSub - 1) / (a.subs * W::kSub);
+    a.mt = FastDiv((uint32_t)mt);
     if (row_tiles * mt > kMostTiles) return MD_ERR_UNSUPPORTED;
     static std::atomic<uint64_t> setup{0};
-    return launch(k_expert_wide<MODE>, W::kThreads, W::smem(a.E), W::smem(MD_MAX_EXPERTS), setup, row_tiles * mt, 2, ma,
-                  mb, a, s);
+    return launch(k_expert_wide<MODE>, W::kThreads, W::smem(a.E), W::smem(MD_MAX_EXPERTS), setup, row_tiles * mt, 2, s, ma,
+                  mb, mb, a);
 }
 
 // Few rows to an expert: narrow tiles leave shared memory for a deep ring,
@@ -1197,13 +1213,18 @@ extern "C" int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int 
     a.polls = md::hook_poll_limit(kPolls);
     a.y = dw;
     using W = Wide<kWgrad>;
-    CUtensorMap ma, mb;
-    if (!md::make_map(&ma, dy, kBf16, 2, N, rows, 0, 64, 64) || !md::make_map(&mb, x, kBf16, 2, K, rows, 0, 64, 64))
+    CUtensorMap ma, mb, mo;
+    if (!md::make_map(&ma, dy, kBf16, 2, N, rows, 0, 64, 64) || !md::make_map(&mb, x, kBf16, 2, K, rows, 0, 64, 64) ||
+        !md::make_map(&mo, dw, a.out_bf16 ? kBf16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, size, K, N, E, 64 / size, 32,
+                      CU_TENSOR_MAP_SWIZZLE_64B))
         return MD_ERR_CUDA;
     const int64_t across = (K + 255) / 256;
     a.subs = subs_for(E * across * ((N + W::kSub - 1) / W::kSub));
-    const int64_t tiles = E * across * ((N + a.subs * W::kSub - 1) / (a.subs * W::kSub));
+    const int64_t mt = (N + a.subs * W::kSub - 1) / (a.subs * W::kSub), tiles = E * across * mt;
     if (tiles > kMostTiles) return MD_ERR_UNSUPPORTED;
+    a.mt = FastDiv((uint32_t)mt);
+    a.per = FastDiv((uint32_t)(mt * across));
     static std::atomic<uint64_t> setup{0};
-    return launch(k_expert_wide<kWgrad>, W::kThreads, W::smem(E), W::smem(MD_MAX_EXPERTS), setup, tiles, 2, ma, mb, a, s);
+    return launch(k_expert_wide<kWgrad>, W::kThreads, W::smem(E), W::smem(MD_MAX_EXPERTS), setup, tiles, 2, s, ma, mb,
+                  mo, a);
 }
