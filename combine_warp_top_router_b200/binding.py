@@ -93,6 +93,8 @@ class MoeDispatchError(RuntimeError):
 def lib():
     """The loaded libmoedispatch.so; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -135,7 +137,8 @@ def _call(name: str, dev, *args) -> int:
     scratch array) for that device, so tensors on another device are handled
     by making their device current for the call."""
     fn = getattr(lib(), name)
-    dev = torch.device(dev)
+    if type(dev) is not torch.device:
+        dev = torch.device(dev)
     if dev.index is None or torch.cuda.current_device() == dev.index:
         return fn(*args)
     with torch.cuda.device(dev):
@@ -592,20 +595,47 @@ def md_token_shuffle_pair(idx_prev, idx_l, C, C2, expert_to_rank_next, R, min_ob
 
 # ------------------------------------------------------- experts
 
-def _matrix(t, name, shape):
-    """A tensor of exactly this shape (None: any extent)."""
-    if t.dim() != len(shape) or any(want is not None and have != want
-                                    for have, want in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
-                         f"{['any' if s is None else s for s in shape]}")
-    return t
+# A call for a few rows takes about as long on the host as on the GPU, so the checks
+# below look at everything at once and ask what is wrong only if something is.
+
+def _first(t, name, dtype, dims):
+    """A call's first tensor: it names the device."""
+    _need(t, name, dtype)
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    return t.device
 
 
-def _groups(expert_offsets, expert_counts, E, dev):
-    _need(expert_offsets, "expert_offsets", torch.int32, dev)
-    _need(expert_counts, "expert_counts", torch.int32, dev)
-    _room(expert_offsets, "expert_offsets", E)
-    _room(expert_counts, "expert_counts", E)
+def _exact(t, name, dtype, dev, shape):
+    """A contiguous tensor of this type, device and shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, dtype, dev)
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _words(t, name, dev, n):
+    """A contiguous int32 tensor of n elements or more."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == dev
+            and t.numel() >= n and t.is_contiguous()):
+        _need(t, name, torch.int32, dev)
+        _room(t, name, n)
+
+
+def _tail(dev_status, stream, dev):
+    """The addresses of the last two arguments of every entry point."""
+    if dev_status is not None:
+        _words(dev_status, "dev_status", dev, 1)
+        dev_status = dev_status.data_ptr()
+    if stream is not None:
+        return dev_status, stream.cuda_stream
+    if _raw_stream is not None:
+        return dev_status, _raw_stream(dev.index)
+    return dev_status, torch.cuda.current_stream(dev).cuda_stream
+
+
+# the current stream's handle without the Stream object around it (2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def md_expert_gemm(x, w, expert_offsets, expert_counts, w_layout=MD_W_NK, out=None,
@@ -614,20 +644,23 @@ def md_expert_gemm(x, w, expert_offsets, expert_counts, w_layout=MD_W_NK, out=No
 
     Rows are expert-grouped: expert_offsets and expert_counts come from md_dispatch_layout.
     Rows of no expert are left untouched in `out`."""
-    _need(x, "x", torch.bfloat16)
-    dev = x.device
-    _need(w, "w", torch.bfloat16, dev)
-    if w_layout not in (MD_W_NK, MD_W_KN):
+    dev = _first(x, "x", torch.bfloat16, 2)
+    if w_layout != MD_W_NK and w_layout != MD_W_KN:
         raise ValueError("w_layout must be MD_W_NK or MD_W_KN")
-    rows, K = _matrix(x, "x", (None, None)).shape
-    _matrix(w, "w", (None, None, K) if w_layout == MD_W_NK else (None, K, None))
+    _need(w, "w", torch.bfloat16, dev)
+    rows, K = x.shape
+    if w.dim() != 3 or w.shape[2 if w_layout == MD_W_NK else 1] != K:
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected three dimensions and K = {K}")
     E, N = w.shape[0], w.shape[1 if w_layout == MD_W_NK else 2]
-    _groups(expert_offsets, expert_counts, E, dev)
+    _words(expert_offsets, "expert_offsets", dev, E)
+    _words(expert_counts, "expert_counts", dev, E)
     if out is None:
-        out = torch.empty(rows, N, dtype=torch.bfloat16, device=dev)
-    _matrix(_need(out, "out", torch.bfloat16, dev), "out", (rows, N))
-    rc = _call("md_expert_gemm", dev, _ptr(x), rows, K, _ptr(w), E, N, w_layout, _ptr(expert_offsets),
-               _ptr(expert_counts), _ptr(out), _ptr(dev_status), _stream(stream, dev))
+        out = x.new_empty((rows, N))
+    else:
+        _exact(out, "out", torch.bfloat16, dev, (rows, N))
+    status, stream = _tail(dev_status, stream, dev)
+    rc = _call("md_expert_gemm", dev, x.data_ptr(), rows, K, w.data_ptr(), E, N, w_layout,
+               expert_offsets.data_ptr(), expert_counts.data_ptr(), out.data_ptr(), status, stream)
     _check(rc, "md_expert_gemm")
     return out
 
@@ -636,32 +669,36 @@ def md_expert_gated(x, w, expert_offsets, expert_counts, keep=False, out=None, c
                     scales=None, dev_status=None, stream=None):
     """Gated up-projection act = silu(g) * u with g, u = x w[e]^T; w [E, 2F, K] holds g's rows, then u's.
 
-    keep=True (or codes and scales given) also writes the 8-bit checkpoint of g and u that
+    keep=True (or codes or scales given) also writes the 8-bit checkpoint of g and u that
     md_expert_gated_backward reads, and returns (act, codes, scales)."""
-    _need(x, "x", torch.bfloat16)
-    dev = x.device
+    dev = _first(x, "x", torch.bfloat16, 2)
     _need(w, "w", torch.bfloat16, dev)
-    rows, K = _matrix(x, "x", (None, None)).shape
-    E, N, _ = _matrix(w, "w", (None, None, K)).shape
-    if N % 2:
-        raise ValueError("w must hold as many rows for g as for u")
+    rows, K = x.shape
+    if w.dim() != 3 or w.shape[2] != K or w.shape[1] % 2:
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected [E, 2F, {K}]")
+    E, N = w.shape[0], w.shape[1]
     F = N // 2
-    _groups(expert_offsets, expert_counts, E, dev)
+    _words(expert_offsets, "expert_offsets", dev, E)
+    _words(expert_counts, "expert_counts", dev, E)
     if out is None:
-        out = torch.empty(rows, F, dtype=torch.bfloat16, device=dev)
-    _matrix(_need(out, "out", torch.bfloat16, dev), "out", (rows, F))
+        out = x.new_empty((rows, F))
+    else:
+        _exact(out, "out", torch.bfloat16, dev, (rows, F))
     keep = keep or codes is not None or scales is not None
     if keep:
         blocks = 2 * -(-F // MD_CHECKPOINT_BLOCK)
         if codes is None:
-            codes = torch.empty(rows, N, dtype=torch.float8_e4m3fn, device=dev)
+            codes = torch.empty((rows, N), dtype=torch.float8_e4m3fn, device=dev)
+        else:
+            _exact(codes, "codes", torch.float8_e4m3fn, dev, (rows, N))
         if scales is None:
-            scales = torch.empty(rows, blocks, dtype=torch.uint8, device=dev)
-        _matrix(_need(codes, "codes", torch.float8_e4m3fn, dev), "codes", (rows, N))
-        _matrix(_need(scales, "scales", torch.uint8, dev), "scales", (rows, blocks))
-    rc = _call("md_expert_gated", dev, _ptr(x), rows, K, _ptr(w), E, F, _ptr(expert_offsets),
-               _ptr(expert_counts), _ptr(out), _ptr(codes), _ptr(scales), _ptr(dev_status),
-               _stream(stream, dev))
+            scales = torch.empty((rows, blocks), dtype=torch.uint8, device=dev)
+        else:
+            _exact(scales, "scales", torch.uint8, dev, (rows, blocks))
+    status, stream = _tail(dev_status, stream, dev)
+    rc = _call("md_expert_gated", dev, x.data_ptr(), rows, K, w.data_ptr(), E, F,
+               expert_offsets.data_ptr(), expert_counts.data_ptr(), out.data_ptr(),
+               codes.data_ptr() if keep else None, scales.data_ptr() if keep else None, status, stream)
     _check(rc, "md_expert_gated")
     return (out, codes, scales) if keep else out
 
@@ -671,11 +708,12 @@ def md_expert_wgrad(dy, x, expert_offsets, expert_counts, out_dtype=torch.float3
     """dw[e] = sum over expert e's rows of dy[r]^T x[r], [E, N, K]; accumulate adds into a float32 dw.
 
     E is the length of expert_counts (or dw's first extent)."""
-    _need(dy, "dy", torch.bfloat16)
-    dev = dy.device
+    dev = _first(dy, "dy", torch.bfloat16, 2)
     _need(x, "x", torch.bfloat16, dev)
-    rows, N = _matrix(dy, "dy", (None, None)).shape
-    _, K = _matrix(x, "x", (rows, None)).shape
+    rows, N = dy.shape
+    if x.dim() != 2 or x.shape[0] != rows:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [{rows}, K]")
+    K = x.shape[1]
     if dw is not None:
         out_dtype = dw.dtype
     if out_dtype not in (torch.float32, torch.bfloat16):
@@ -683,13 +721,17 @@ def md_expert_wgrad(dy, x, expert_offsets, expert_counts, out_dtype=torch.float3
     if accumulate and (dw is None or out_dtype != torch.float32):
         raise ValueError("accumulate needs a float32 dw to add to")
     E = expert_counts.numel() if dw is None else dw.shape[0]
-    _groups(expert_offsets, expert_counts, E, dev)
+    _words(expert_offsets, "expert_offsets", dev, E)
+    _words(expert_counts, "expert_counts", dev, E)
     if dw is None:
-        dw = torch.empty(E, N, K, dtype=out_dtype, device=dev)
-    _matrix(_need(dw, "dw", out_dtype, dev), "dw", (E, N, K))
-    rc = _call("md_expert_wgrad", dev, _ptr(dy), _ptr(x), rows, E, N, K, _ptr(expert_offsets),
-               _ptr(expert_counts), MD_F32 if out_dtype == torch.float32 else MD_BF16,
-               1 if accumulate else 0, _ptr(dw), _ptr(dev_status), _stream(stream, dev))
+        dw = torch.empty((E, N, K), dtype=out_dtype, device=dev)
+    else:
+        _exact(dw, "dw", out_dtype, dev, (E, N, K))
+    status, stream = _tail(dev_status, stream, dev)
+    rc = _call("md_expert_wgrad", dev, dy.data_ptr(), x.data_ptr(), rows, E, N, K,
+               expert_offsets.data_ptr(), expert_counts.data_ptr(),
+               MD_F32 if out_dtype == torch.float32 else MD_BF16, 1 if accumulate else 0,
+               dw.data_ptr(), status, stream)
     _check(rc, "md_expert_wgrad")
     return dw
 
@@ -699,21 +741,21 @@ def md_expert_gated_backward(da, codes, scales, dh=None, act=None, want_act=True
 
     dh [rows, 2F] is the gradient of g, then of u; act is the activation computed again from
     the checkpoint (None with want_act=False)."""
-    _need(da, "da", torch.bfloat16)
-    dev = da.device
-    rows, F = _matrix(da, "da", (None, None)).shape
-    _matrix(_need(codes, "codes", torch.float8_e4m3fn, dev), "codes", (rows, 2 * F))
-    _matrix(_need(scales, "scales", torch.uint8, dev), "scales",
-            (rows, 2 * -(-F // MD_CHECKPOINT_BLOCK)))
+    dev = _first(da, "da", torch.bfloat16, 2)
+    rows, F = da.shape
+    _exact(codes, "codes", torch.float8_e4m3fn, dev, (rows, 2 * F))
+    _exact(scales, "scales", torch.uint8, dev, (rows, 2 * -(-F // MD_CHECKPOINT_BLOCK)))
     if dh is None:
-        dh = torch.empty(rows, 2 * F, dtype=torch.bfloat16, device=dev)
-    if act is None and want_act:
-        act = torch.empty(rows, F, dtype=torch.bfloat16, device=dev)
-    _matrix(_need(dh, "dh", torch.bfloat16, dev), "dh", (rows, 2 * F))
+        dh = da.new_empty((rows, 2 * F))
+    else:
+        _exact(dh, "dh", torch.bfloat16, dev, (rows, 2 * F))
     if act is not None:
-        _matrix(_need(act, "act", torch.bfloat16, dev), "act", (rows, F))
-    rc = _call("md_expert_gated_backward", dev, _ptr(da), _ptr(codes), _ptr(scales), rows, F, _ptr(dh),
-               _ptr(act), _stream(stream, dev))
+        _exact(act, "act", torch.bfloat16, dev, (rows, F))
+    elif want_act:
+        act = da.new_empty((rows, F))
+    _, stream = _tail(None, stream, dev)
+    rc = _call("md_expert_gated_backward", dev, da.data_ptr(), codes.data_ptr(), scales.data_ptr(), rows,
+               F, dh.data_ptr(), None if act is None else act.data_ptr(), stream)
     _check(rc, "md_expert_gated_backward")
     return dh, act
 
@@ -724,26 +766,30 @@ def md_combine_backward(dout, assign_row, topk_w, y=None, y_rows=None, dy=None, 
 
     dw [T, k] is the gates' gradient; it needs the expert outputs y (without y it is None).
     dy has y's rows, or y_rows (default T * k)."""
-    _need(dout, "dout", torch.bfloat16)
-    dev = dout.device
-    _need(assign_row, "assign_row", torch.int32, dev)
+    dev = _first(dout, "dout", torch.bfloat16, 2)
+    T, H = dout.shape
     _need(topk_w, "topk_w", torch.float32, dev)
-    T, H = _matrix(dout, "dout", (None, None)).shape
-    T, k = _matrix(topk_w, "topk_w", (T, None)).shape
-    _matrix(assign_row, "assign_row", (T, k))
+    if topk_w.dim() != 2 or topk_w.shape[0] != T:
+        raise ValueError(f"topk_w has shape {tuple(topk_w.shape)}, expected [{T}, k]")
+    k = topk_w.shape[1]
+    _exact(assign_row, "assign_row", torch.int32, dev, (T, k))
     if y is not None:
-        _matrix(_need(y, "y", torch.bfloat16, dev), "y", (None, H))
         y_rows = y.shape[0]
+        _exact(y, "y", torch.bfloat16, dev, (y_rows, H))
         if dw is None:
-            dw = torch.empty(T, k, dtype=torch.float32, device=dev)
-        _matrix(_need(dw, "dw", torch.float32, dev), "dw", (T, k))
+            dw = topk_w.new_empty((T, k))
+        else:
+            _exact(dw, "dw", torch.float32, dev, (T, k))
     elif dw is not None:
         raise ValueError("dw needs y (the expert outputs)")
     if dy is None:
-        dy = torch.empty(T * k if y_rows is None else y_rows, H, dtype=torch.bfloat16, device=dev)
-    _matrix(_need(dy, "dy", torch.bfloat16, dev), "dy", (y_rows, H))
-    rc = _call("md_combine_backward", dev, _ptr(dout), _ptr(y), dy.shape[0], _ptr(assign_row), _ptr(topk_w),
-               T, k, H, _ptr(dy), _ptr(dw), _ptr(dev_status), _stream(stream, dev))
+        dy = dout.new_empty((T * k if y_rows is None else y_rows, H))
+    else:
+        _exact(dy, "dy", torch.bfloat16, dev, (dy.shape[0] if y_rows is None else y_rows, H))
+    status, stream = _tail(dev_status, stream, dev)
+    rc = _call("md_combine_backward", dev, dout.data_ptr(), None if y is None else y.data_ptr(),
+               dy.shape[0], assign_row.data_ptr(), topk_w.data_ptr(), T, k, H, dy.data_ptr(),
+               None if dw is None else dw.data_ptr(), status, stream)
     _check(rc, "md_combine_backward")
     return dy, dw
 
