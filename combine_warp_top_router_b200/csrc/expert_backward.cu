@@ -5,7 +5,7 @@
 // (the checkpoint's codes in 8-byte ones); they are bound by HBM.
 #include <cuda_fp16.h>
 
-#include "common.cuh"
+#include "activation.cuh"
 
 namespace {
 
@@ -42,40 +42,57 @@ __global__ void __launch_bounds__(kThreads)
                      uint4 *__restrict__ act)
 {
     const int C = F / 8, blocks = (F + kBlock - 1) / kBlock;
-    const int64_t n = rows * C;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t r = i / C;
-        const int c = (int)(i - r * C);
-        const uint4 d4 = md::ld_stream(da + i);
-        const uint8_t *cr = codes + r * 2 * F + c * 8, *sr = scales + r * 2 * blocks + c * 8 / kBlock;
-        const uint2 cg = __ldg(reinterpret_cast<const uint2 *>(cr)), cu = __ldg(reinterpret_cast<const uint2 *>(cr + F));
-        const float sg = scale_of(__ldg(sr)), su = scale_of(__ldg(sr + blocks));
-        float g[8], u[8];
-        from_e4m3(cg.x, sg, g);
-        from_e4m3(cg.y, sg, g + 4);
-        from_e4m3(cu.x, su, u);
-        from_e4m3(cu.y, su, u + 4);
-        const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
-        uint32_t og[4], ou[4], oa[4];
+    const int64_t n = rows * C, step = (int64_t)gridDim.x * kThreads;
+    // two pieces of 8 columns at a time: all their loads are on the way before the first is used
+    for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < n; i0 += 2 * step) {
+        int64_t r[2];
+        int c[2];
+        uint4 d4[2];
+        uint2 cg[2], cu[2];
+        uint32_t sg[2], su[2];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            float vg[2], vu[2], va[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float d = h ? md::bf16hi(dw[p]) : md::bf16lo(dw[p]);
-                const float x = g[2 * p + h], y = u[2 * p + h];
-                const float s = 1.0f / (1.0f + expf(-x));
-                vg[h] = d * y * s * (1.0f + x * (1.0f - s));
-                vu[h] = d * x * s;
-                va[h] = x * s * y;
-            }
-            og[p] = md::pack_bf16x2(vg[0], vg[1]);
-            ou[p] = md::pack_bf16x2(vu[0], vu[1]);
-            oa[p] = md::pack_bf16x2(va[0], va[1]);
+        for (int q = 0; q < 2; ++q) {
+            const int64_t i = i0 + q * step < n ? i0 + q * step : i0;
+            r[q] = i / C;
+            c[q] = (int)(i - r[q] * C);
+            const uint8_t *cr = codes + r[q] * 2 * F + c[q] * 8, *sr = scales + r[q] * 2 * blocks + c[q] * 8 / kBlock;
+            d4[q] = md::ld_stream(da + i);
+            cg[q] = __ldg(reinterpret_cast<const uint2 *>(cr));
+            cu[q] = __ldg(reinterpret_cast<const uint2 *>(cr + F));
+            sg[q] = __ldg(sr);
+            su[q] = __ldg(sr + blocks);
         }
-        md::st_stream(dh + r * 2 * C + c, make_uint4(og[0], og[1], og[2], og[3]));
-        md::st_stream(dh + r * 2 * C + C + c, make_uint4(ou[0], ou[1], ou[2], ou[3]));
-        if (act) md::st_stream(act + i, make_uint4(oa[0], oa[1], oa[2], oa[3]));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (i0 + q * step >= n) break;
+            float g[8], u[8];
+            from_e4m3(cg[q].x, scale_of(sg[q]), g);
+            from_e4m3(cg[q].y, scale_of(sg[q]), g + 4);
+            from_e4m3(cu[q].x, scale_of(su[q]), u);
+            from_e4m3(cu[q].y, scale_of(su[q]), u + 4);
+            const uint32_t dw[4] = {d4[q].x, d4[q].y, d4[q].z, d4[q].w};
+            uint32_t og[4], ou[4], oa[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                float vg[2], vu[2], va[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float d = h ? md::bf16hi(dw[p]) : md::bf16lo(dw[p]);
+                    const float x = g[2 * p + h], y = u[2 * p + h];
+                    const float s = md::sigmoid(x);
+                    vg[h] = d * y * s * (1.0f + x * (1.0f - s));
+                    vu[h] = d * x * s;
+                    va[h] = x * s * y;
+                }
+                og[p] = md::pack_bf16x2(vg[0], vg[1]);
+                ou[p] = md::pack_bf16x2(vu[0], vu[1]);
+                oa[p] = md::pack_bf16x2(va[0], va[1]);
+            }
+            uint4 *to = dh + r[q] * 2 * C + c[q];
+            md::st_stream(to, make_uint4(og[0], og[1], og[2], og[3]));
+            md::st_stream(to + C, make_uint4(ou[0], ou[1], ou[2], ou[3]));
+            if (act) md::st_stream(act + r[q] * C + c[q], make_uint4(oa[0], oa[1], oa[2], oa[3]));
+        }
     }
 }
 

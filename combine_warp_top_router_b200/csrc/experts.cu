@@ -23,6 +23,7 @@
 // wait runs out raises the CTA's abort flag and MD_ERR_TIMEOUT, all roles leave
 // their loops, copies and MMAs in flight are awaited (bounded again), TMEM is
 // freed, and the kernel returns.
+#include "activation.cuh"
 #include "tcgen05.cuh"
 
 namespace {
@@ -257,22 +258,6 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
     return r;
 }
 
-// g / (1 + exp(-g)) * u.  exp(-g) = 2^t with t = -g log2(e); t's rounding error,
-// which would be |g| 2^-24 of the result, is put back to first order, so the result
-// is good to a few float32 ulps for |g| < 44 and to 2^-17 of itself beyond
-// (where exp overflows, it is 0).
-__device__ __forceinline__ float silu_times(float g, float u)
-{
-    constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
-    const float t = -g * kLog2e;
-    const float lost = fabsf(t) < 64.0f ? fmaf(-g, kLog2e, -t) * kLn2 : 0.0f;
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    e = lost == 0.0f ? e : fmaf(e, lost, e);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return g * r * u;
-}
-
 // Eight columns of one row and one half of the checkpoint.  The four lanes of
 // a 32-column block share its scale: the smallest 2^s with amax <= 448 * 2^s.
 // 448 = 1.75 * 2^8, so s follows from amax's exponent and whether its fraction
@@ -367,7 +352,8 @@ __device__ __forceinline__ void emit(const uint32_t (&v)[32], int c, const Tile 
                 uint32_t w[4];
 #pragma unroll
                 for (int p = 0; p < 4; ++p)
-                    w[p] = md::pack_bf16x2(silu_times(g[2 * p], u[2 * p]), silu_times(g[2 * p + 1], u[2 * p + 1]));
+                    w[p] = md::pack_bf16x2(g[2 * p] * md::sigmoid(g[2 * p]) * u[2 * p],
+                                           g[2 * p + 1] * md::sigmoid(g[2 * p + 1]) * u[2 * p + 1]);
                 *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + r * a.pitch + f0) =
                     make_uint4(w[0], w[1], w[2], w[3]);
             }
