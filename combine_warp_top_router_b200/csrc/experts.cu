@@ -599,17 +599,21 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
 // each CTA.  For such a block the second CTA awaits its loads on a barrier of
 // its own, clears, and tells the first; passing every stage on this way took a
 // quarter of the loads' rate.  The tensor cores drop low bits at each
-// addition: over thousands of rows the sums drift by 1.6e-6.  float32 results are
-// therefore summed in TMEM over kSegment blocks at most and then added in dw.
-constexpr int kSegment = 32;
+// addition: summed whole, 131072 rows over 128 experts are off by 1.6e-6 (2-norm).  float32
+// results are therefore summed in TMEM over kSegment blocks at most, in equal shares, and
+// then added in dw, in order: 0.9e-6, for 5% of the time.  (32 blocks: 1.1e-6.)
+constexpr int kSegment = 18;
 
 template <int MODE>
 struct Wide {
     static constexpr int kPart = 128 * kTileK * 2;  // 16 KB: 128 rows of A, or half of the tile's x rows
-    static constexpr int kParts = 12;               // 4 stages of three, or 6 of two (one sub)
+    // 4 stages of three parts, or 6 of two (one sub).  Weight gradient: 3 or 4, and two buffers of
+    // 4 KB a warp for dw in the rest.
+    static constexpr int kParts = MODE == kWgrad ? 9 : 12;
+    static constexpr int kStaging = MODE == kWgrad ? kEpiWarps * 8192 : kStagingBytes;
     static constexpr int kThreads = 32 * 12;
     static constexpr int kSub = MODE == kGated ? 128 : 256;  // output columns of a sub
-    static size_t smem(int E) { return 1024 + (size_t)kParts * kPart + kStagingBytes + Table::bytes(E); }
+    static size_t smem(int E) { return 1024 + (size_t)kParts * kPart + kStaging + Table::bytes(E); }
 };
 
 struct WideBars {
@@ -626,40 +630,42 @@ __device__ __forceinline__ int blocks_at(int i, int kb, int subs)
     return subs == 2 && kb - i >= 2 && (i == 0 || i == kb - 2) ? 2 : 1;
 }
 
-// 32 columns of dw's rows, one row in each lane of the warp, through the warp's 2 KB of
-// staging in boxes of 32 rows by 64 bytes, stored (or added) by TMA: its engine does not
-// hold up the warp, which has the next accumulator to empty, and the map cuts the
-// box at dw's edges.  Stores straight from registers touch 32 lines each; they
-// reached 4.2 TB/s and held sub 1's accumulator for 8000 cycles.
-__device__ __forceinline__ void put_rows(const uint32_t (&v)[32], const CUtensorMap *map, const Args &a, int c, int row0,
-                                         int e, bool add, unsigned char *st)
+// 32 columns of dw's rows, one row in each lane of the warp, into one of the warp's two
+// 4 KB buffers: 32 rows of 128 bytes in the map's swizzle, which hold 32 float32
+// columns or two runs of bf16 ones.
+__device__ __forceinline__ void fill_rows(const uint32_t (&v)[32], const Args &a, bool odd, unsigned char *st)
 {
-    const int lane = threadIdx.x & 31, sw = (lane >> 1 & 3) * 16;  // the map's 64-byte swizzle
+    const int lane = threadIdx.x & 31, sw = (lane & 7) * 16;
+    unsigned char *row = st + lane * 128;
+    if (a.out_bf16) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t w[16];
-        if (a.out_bf16) {
-            if (h == 1) break;
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = md::pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-        } else {
-            if (c + 16 * h >= a.k) break;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = v[16 * h + i];
+            for (int h = 0; h < 4; ++h)
+                w[h] = md::pack_bf16x2(__uint_as_float(v[8 * i + 2 * h]), __uint_as_float(v[8 * i + 2 * h + 1]));
+            *reinterpret_cast<uint4 *>(row + ((i * 16 + (odd ? 64 : 0)) ^ sw)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        md::bulk_wait_read<0>();  // lane 0's store that read the buffer; the others have none
-        __syncwarp();
+        return;
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4 *>(st + lane * 64 + (i * 16 ^ sw)) =
-                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        md::fence_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-            if (add) md::tma_add_3d(map, md::smem_addr(st), c + 16 * h, row0, e);
-            else md::tma_store_3d(map, md::smem_addr(st), c + 16 * h, row0, e);
-            md::bulk_commit();
-        }
+    for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4 *>(row + (i * 16 ^ sw)) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
+// The filled buffer to dw, stored or added by TMA: the map cuts the box at dw's edges, and the
+// warp goes on to the next columns.  Rows of 128 bytes: where dw's rows are not a multiple
+// of 32 bytes long, each box row ends in parts of sectors, and with 64-byte rows the
+// stores took twice the time.  Plain stores, from registers (32 lines each) or
+// turned around in shared memory, were slower: the warp's own time.
+__device__ __forceinline__ void send_rows(const CUtensorMap *map, int c, int row0, int e, bool add, const unsigned char *st)
+{
+    md::fence_async_shared();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        if (add) md::tma_add_3d(map, md::smem_addr(st), c, row0, e);
+        else md::tma_store_3d(map, md::smem_addr(st), c, row0, e);
+        md::bulk_commit();
     }
 }
 
@@ -679,7 +685,7 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
     // an offset, not a rounded address: the compiler then knows shared memory as such
     unsigned char *base = smem_raw + (-md::smem_addr(smem_raw) & 1023u);
     unsigned char *staging = base + W::kParts * W::kPart;
-    const Table tab(staging + kStagingBytes, a.E);
+    const Table tab(staging + W::kStaging, a.E);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = (int)md::cluster_rank();
 
@@ -742,8 +748,12 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
     };
     // blocks of the tile's contraction
     auto blocks_of = [&](const Tile &q) { return ((kWg ? q.count : a.k) + kTileK - 1) / kTileK; };
-    // blocks that one accumulator sums
-    const int segment = kWg && !a.out_bf16 ? kSegment : INT32_MAX;
+    // blocks that one accumulator sums: all, or an equal share of kSegment at most
+    auto segment_of = [&](int blocks) {
+        if (!kWg || a.out_bf16 || blocks <= kSegment) return blocks;
+        const int parts = (blocks + kSegment - 1) / kSegment;
+        return (blocks + parts - 1) / parts;
+    };
 
     if (warp >= kEpiWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -859,6 +869,7 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                     const Tile q = tile_of(t);
                     const int subs = q.subs, blocks = blocks_of(q);
                     const uint32_t idesc = md::mma_desc(256, q.n, !kAKMajor, kWg);
+                    const int segment = segment_of(blocks);
                     for (int from = 0, kb; ok && from < blocks; from += kb, opened += subs) {
                         kb = min(blocks - from, segment);
                         // block i of one sub, in stage s; of a last block as many sixteenths as hold rows
@@ -918,20 +929,20 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
         constexpr int kRun = kWg ? 32 : 64;
         const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + group * (kWg ? 128 : 32);
         uint32_t acc = 0;
+        int buffer = 0;  // weight gradient: of the warp's two
         bool ok = true;
-        // this warp's columns of an accumulator, in four runs of 32, into registers (all of them,
-        // the tile's or not: a register that is loaded on a condition stays taken throughout)
-        auto take = [&](uint32_t (&v)[4][32], bool empty) __attribute__((always_inline)) {
-            if (kWg && empty) {  // an expert without rows
-#pragma unroll
-                for (int i = 0; i < 128; ++i) v[i >> 5][i & 31] = 0;
-                return;
-            }
+        // Accumulators are taken in turn: wait for the next, read this warp's columns in runs of 32,
+        // give it back.  (All runs are read, the tile's or not: a register that is loaded on a
+        // condition stays taken throughout.)
+        auto await = [&]() {
             ok = epilogue_wait(&b->tfull[acc & 1], (acc >> 1) & 1u, sh, a);
-            if (!ok) return;
             md::tmem_fence_after();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) md::tmem_ld32(v[i], mine + (acc & 1) * BN + i * kRun);
+            return ok;
+        };
+        auto read = [&](uint32_t (&v)[32], int run) __attribute__((always_inline)) {
+            md::tmem_ld32(v, mine + (acc & 1) * BN + run * kRun);
+        };
+        auto give_back = [&]() {
             md::tmem_ld_wait();
             md::tmem_fence_before();
             __syncwarp();
@@ -940,19 +951,25 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
             if (lane == 0) md::mbar_arrive_cluster_relaxed(md::map_rank(md::smem_addr(&b->tempty[acc & 1]), 0));
             ++acc;
         };
+        auto take = [&](uint32_t (&v)[4][32]) __attribute__((always_inline)) {
+            if (!await()) return;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) read(v[i], i);
+            give_back();
+        };
         // the subs' accumulators, out through put(values, sub, run).  Sub 1's is taken as soon as
         // put's own registers allow: a spilled value would come back from L2, under all that
         // traffic some 1500 cycles a load.
         constexpr int kBefore = MODE == kGated ? 3 : 2;
         auto results = [&](int subs, auto put) __attribute__((always_inline)) {
             uint32_t v[4][32];
-            take(v, false);
+            take(v);
             if (!ok) return;
 #pragma unroll
             for (int i = 0; i < kBefore; ++i) put(v[i], 0, i);
             if (subs == 2) {
                 uint32_t w[4][32];
-                take(w, false);
+                take(w);
                 if (!ok) return;
 #pragma unroll
                 for (int i = kBefore; i < 4; ++i) put(v[i], 0, i);
@@ -971,21 +988,31 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
             if (kWg) {
                 const int blocks = blocks_of(q), cols = min(a.k - q.c0, BN);
                 if (blocks == 0 && a.accumulate) continue;
-                for (int from = 0; from == 0 || (ok && from < blocks); from += min(segment, max(blocks - from, 1))) {  // once if empty
+                const int segment = max(segment_of(blocks), 1);
+                for (int from = 0; from == 0 || (ok && from < blocks); from += segment) {  // once if empty
                     const bool add = a.accumulate || from > 0;
                     if (from > 0) md::bulk_wait_all();  // what this adds to is written
                     auto put = [&](const uint32_t (&x)[32], int sub, int i) __attribute__((always_inline)) {
                         const int c = group * 128 + i * 32, row0 = q.m0 + sub * W::kSub + (warp & 3) * 32;
-                        if (c < cols && row0 < a.n) put_rows(x, &map_d, a, q.c0 + c, row0, q.e, add, staging + warp * 2048);
+                        if (c >= cols || row0 >= a.n) return;
+                        unsigned char *st = staging + warp * 8192 + buffer;
+                        const bool pair = a.out_bf16, odd = pair && (i & 1);
+                        if (!odd) {  // the buffer's last store has read it (lane 0's group; the others have none)
+                            md::bulk_wait_read<1>();
+                            __syncwarp();
+                        }
+                        fill_rows(x, a, odd, st);
+                        if (pair && !odd && c + 32 < cols) return;  // with the next run
+                        send_rows(&map_d, q.c0 + c - (odd ? 32 : 0), row0, q.e, add, st);
+                        buffer ^= 4096;  // with each store made: a tile's edge may leave some out
                     };
+if (blocks == 0) {  // an expert without rows
+                        uint32_t none[32] = {};
 #pragma unroll 1
-                    for (int sub = 0; ok && sub < subs; ++sub) {
-                        uint32_t v[4][32];
-                        take(v, blocks == 0);
-                        if (!ok) break;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) put(v[i], sub, i);
+                        for (int i = 0; i < 4 * subs; ++i) put(none, i >> 2, i & 3);
+                        break;
                     }
+                    results(subs, put);
                 }
             } else {
                 auto put = [&](const uint32_t (&x)[32], int sub, int i) __attribute__((always_inline)) {
@@ -1201,8 +1228,7 @@ extern "C" int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int 
     using W = Wide<kWgrad>;
     CUtensorMap ma, mb, mo;
     if (!md::make_map(&ma, dy, kBf16, 2, N, rows, 0, 64, 64) || !md::make_map(&mb, x, kBf16, 2, K, rows, 0, 64, 64) ||
-        !md::make_map(&mo, dw, a.out_bf16 ? kBf16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, size, K, N, E, 64 / size, 32,
-                      CU_TENSOR_MAP_SWIZZLE_64B))
+        !md::make_map(&mo, dw, a.out_bf16 ? kBf16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, size, K, N, E, 128 / size, 32))
         return MD_ERR_CUDA;
     const int64_t across = (K + 255) / 256;
     a.subs = subs_for(E * across * ((N + W::kSub - 1) / W::kSub));

@@ -35,10 +35,10 @@ inline EncodeTiledFn encode_tiled()
 }
 
 // Map of a dense [d2][d1][d0] array (d2 = 0: two dimensions) read or written in
-// boxes of b1 rows of b0 elements with a swizzle of b0 elements' bytes (128 or
-// 64).  Reads outside give zeros, writes outside are dropped.
+// boxes of b1 rows of b0 elements with the 128-byte swizzle; b0 elements span
+// 128 bytes.  Reads outside give zeros, writes outside are dropped.
 inline bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, int esize, int64_t d0,
-                     int64_t d1, int64_t d2, int b0, int b1, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
+                     int64_t d1, int64_t d2, int b0, int b1)
 {
     EncodeTiledFn f = encode_tiled();
     if (!f) return false;
@@ -47,7 +47,7 @@ inline bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType type,
     const cuuint32_t box[3] = {(cuuint32_t)b0, (cuuint32_t)b1, 1u};
     const cuuint32_t one[3] = {1u, 1u, 1u};
     return f(m, type, d2 ? 3u : 2u, const_cast<void *>(base), dims, strides, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
