@@ -1107,8 +1107,14 @@ int run_few(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int
                   mb, a);
 }
 
-// Two subs to a tile where that still gives every pair of SMs several tiles.
-inline int subs_for(int64_t tiles_of_one) { return tiles_of_one >= 4 * md::sm_count() ? 2 : 1; }
+// Two subs to a tile where that still gives the pairs of SMs several tiles each: from four
+// tiles of one sub to a pair (16 experts of 384 rows, 2048 x 2048, one sub / two: 53 / 47 us; of
+// 256 rows 36 / 37; 8 experts of 512 rows, 2048 x 1024: 19 / 28), for the weight gradient
+// from eight (8 experts of 256 rows, 2048 x 2048: 32 / 37; 16 of 512 rows 86 / 79).
+inline int subs_for(int64_t tiles_of_one, int to_a_pair)
+{
+    return tiles_of_one >= (int64_t)to_a_pair * (md::sm_count() / 2) ? 2 : 1;
+}
 
 template <int MODE>
 int run_wide(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int64_t d1, cudaStream_t s)
@@ -1119,7 +1125,7 @@ int run_wide(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, in
         !md::make_map(&mb, x, kBf16, 2, a.k, rows, 0, 64, 64))
         return MD_ERR_CUDA;
     const int64_t row_tiles = rows / 256 + (rows < a.E ? rows : a.E);  // at most
-    a.subs = subs_for(row_tiles * ((a.n + W::kSub - 1) / W::kSub));
+    a.subs = subs_for(row_tiles * ((a.n + W::kSub - 1) / W::kSub), 4);
     const int mt = (a.n + a.subs * W::kSub - 1) / (a.subs * W::kSub);
     a.mt = FastDiv((uint32_t)mt);
     if (row_tiles * mt > kMostTiles) return MD_ERR_UNSUPPORTED;
@@ -1128,9 +1134,17 @@ int run_wide(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, in
                   mb, mb, a);
 }
 
-// Few rows to an expert: narrow tiles leave shared memory for a deep ring,
-// since such a call is bound by reading the weights.  Many: k_expert_wide.
-bool few_rows(int64_t rows, int E) { return rows <= (int64_t)48 * E; }
+// Which form.  With 64 rows to an expert and fewer a call is bound by reading the
+// weights, and k_expert_few's deeper ring of weights does that better; above, its narrow tiles
+// read them again for every 64 rows (64 experts of 2048 x 2048, us, few / wide: 16 rows 84 / 91,
+// 64 rows 91 / 98, 96 rows 108 / 101, 256 rows 227 / 128).  A call with no more wide tiles
+// than there are SM pairs takes the narrow ones at any length (8 experts of 256
+// rows, 1024 x 1024: 11 / 13; of 512 rows 18 / 13).  `sub`: output columns of a wide tile.
+bool few_rows(int64_t rows, int E, int64_t columns, int sub)
+{
+    const int64_t wide = (rows / 256 + (rows < E ? rows : E)) * ((columns + sub - 1) / sub);
+    return rows <= (int64_t)64 * E || wide <= md::sm_count() / 2;
+}
 
 }  // namespace
 
@@ -1158,10 +1172,10 @@ extern "C" int md_expert_gemm(const void *x, int64_t rows, int K, const void *w,
     a.status = dev_status;
     a.polls = md::hook_poll_limit(kPolls);
     if (w_layout == MD_W_NK)
-        return few_rows(rows, E) ? run_few<kNK>(x, w, rows, a, K, N, s)
-                                 : run_wide<kNK>(x, w, rows, a, K, N, s);
-    return few_rows(rows, E) ? run_few<kKN>(x, w, rows, a, N, K, s)
-                             : run_wide<kKN>(x, w, rows, a, N, K, s);
+        return few_rows(rows, E, N, Wide<kNK>::kSub) ? run_few<kNK>(x, w, rows, a, K, N, s)
+                                                     : run_wide<kNK>(x, w, rows, a, K, N, s);
+    return few_rows(rows, E, N, Wide<kKN>::kSub) ? run_few<kKN>(x, w, rows, a, N, K, s)
+                                                 : run_wide<kKN>(x, w, rows, a, N, K, s);
 }
 
 extern "C" int md_expert_gated(const void *x, int64_t rows, int K, const void *w, int E, int F,
@@ -1190,8 +1204,8 @@ extern "C" int md_expert_gated(const void *x, int64_t rows, int K, const void *w
     a.scales = scales;
     a.status = dev_status;
     a.polls = md::hook_poll_limit(kPolls);
-    return few_rows(rows, E) ? run_few<kGated>(x, w, rows, a, K, 2 * (int64_t)F, s)
-                             : run_wide<kGated>(x, w, rows, a, K, 2 * (int64_t)F, s);
+    return few_rows(rows, E, F, Wide<kGated>::kSub) ? run_few<kGated>(x, w, rows, a, K, 2 * (int64_t)F, s)
+                                                    : run_wide<kGated>(x, w, rows, a, K, 2 * (int64_t)F, s);
 }
 
 extern "C" int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int E, int N, int K,
@@ -1231,7 +1245,7 @@ extern "C" int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int 
         !md::make_map(&mo, dw, a.out_bf16 ? kBf16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, size, K, N, E, 128 / size, 32))
         return MD_ERR_CUDA;
     const int64_t across = (K + 255) / 256;
-    a.subs = subs_for(E * across * ((N + W::kSub - 1) / W::kSub));
+    a.subs = subs_for(E * across * ((N + W::kSub - 1) / W::kSub), 8);
     const int64_t mt = (N + a.subs * W::kSub - 1) / (a.subs * W::kSub), tiles = E * across * mt;
     if (tiles > kMostTiles) return MD_ERR_UNSUPPORTED;
     a.mt = FastDiv((uint32_t)mt);

@@ -99,6 +99,140 @@ def test_gemm(counts, K, N, layout):
     close(y, want, mags, K, owned(rows, spans))
 
 
+@pytest.mark.parametrize("op", ["nk", "kn", "gated"])
+@pytest.mark.parametrize("counts,K,N", [
+    ([500] + [0] * 62 + [3], 200, 136),      # the few-row form with several tiles to an expert
+    ([1, 0, 2], 2056, 264),                  # a contraction shared by four CTAs, its blocks uneven
+    ([0, 64, 1, 0], 1000, 136), ([40] * 8, 1032, 256),
+    ([1] * 200 + [0] * 823 + [7], 72, 64),   # as many experts as there may be
+    ([90] * 7 + [0] * 1017, 64, 72), ([300] * 80, 64, 1032)])
+def test_forms_are_exact_on_small_integers(counts, K, N, op):
+    off, cnt, rows, spans = groups(counts, seed=6, gap=1)
+    E, mine, nk = len(counts), None, op != "kn"
+    mine = owned(rows, spans)
+    st = md.new_status(DEV)
+    x = ints(1, rows, K, hi=1)
+    if op == "gated":
+        w = ints(2, E, 2 * N, K, hi=1)
+        act, codes, scales = md.md_expert_gated(x, w, off, cnt, keep=True, dev_status=st)
+        md.check_status(st)
+        h, _ = products64(x, w, spans)
+        g, u = h.chunk(2, 1)
+        want = g * torch.sigmoid(g) * u
+        # exact sums; the activation's float32 steps (8 * 2^-23) and one rounding
+        tol = (2.0 ** -8 + 8 * 2.0 ** -23) * want.abs() + 1e-37
+        assert not bool((((act.double() - want).abs() > tol) & mine[:, None]).any())
+        for have, true in zip(restore64(codes, scales, N), (g, u)):
+            stored, _ = stored64(true[mine])
+            assert torch.equal(have[mine], stored)
+        return
+    w = ints(2, *((E, N, K) if nk else (E, K, N)), hi=1)
+    y = md.md_expert_gemm(x, w, off, cnt, md.MD_W_NK if nk else md.MD_W_KN, dev_status=st)
+    md.check_status(st)
+    want, _ = products64(x, w, spans, nk)
+    assert torch.equal(y[mine], want[mine].to(torch.bfloat16))
+
+
+def test_wgrad_with_the_most_experts():
+    counts = [1] * 200 + [0] * 823 + [130]
+    off, cnt, rows, spans = groups(counts, seed=2)
+    dy, x = ints(1, rows, 72), ints(2, rows, 40)
+    dw = md.md_expert_wgrad(dy, x, off, cnt)
+    want = torch.zeros(1024, 72, 40, dtype=torch.float64, device=DEV)
+    for e, o, c in spans:
+        want[e] = dy[o:o + c].double().t() @ x[o:o + c].double()
+    assert torch.equal(dw.double(), want)
+
+
+def test_gradients_are_the_products_differences():
+    """The products are linear: <dy, x (w + d)^T - x w^T> = <dw, d> and <dy, (x + d) w^T - x w^T> =
+    <dx, d>, exactly on small integers (all sums below 2^24, the outputs below 2^8)."""
+    counts, K, N = [33, 0, 70, 5], 64, 72
+    off, cnt, rows, _ = groups(counts)
+    x, w, dy = ints(1, rows, K, hi=1), ints(2, 4, N, K, hi=1), ints(3, rows, N, hi=1)
+    y = md.md_expert_gemm(x, w, off, cnt).double()
+    for seed in (4, 5):
+        d = (ints(seed, 4, N, K, hi=1) * (torch.rand(4, N, K, device=DEV) < 0.05)).to(torch.bfloat16)
+        step = md.md_expert_gemm(x, w + d, off, cnt).double() - y
+        dw = md.md_expert_wgrad(dy, x, off, cnt).double()
+        assert float((dy.double() * step).sum()) == float((dw * d.double()).sum())
+        d = (ints(seed, rows, K, hi=1) * (torch.rand(rows, K, device=DEV) < 0.05)).to(torch.bfloat16)
+        step = md.md_expert_gemm(x + d, w, off, cnt).double() - y
+        dx = md.md_expert_gemm(dy, w, off, cnt, md.MD_W_KN).double()
+        assert float((dy.double() * step).sum()) == float((dx * d.double()).sum())
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+
+def _far(rows, counts):
+    """Two experts, the second at the very end of `rows`."""
+    t = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    return t([0, rows - counts[1], rows]), t(counts)
+
+
+def test_far_rows_of_x_and_y():
+    rows, wide, c = 270000, 8192, 90
+    off, cnt = _far(rows, [c, c])
+    last = slice(rows - c, rows)
+    x = torch.zeros(rows, wide, dtype=torch.bfloat16, device=DEV)  # 2.2e9 elements
+    x[last] = ints(1, c, wide, hi=1)
+    w = ints(2, 2, 64, wide, hi=1)
+    y = md.md_expert_gemm(x, w, off, cnt)
+    assert torch.equal(y[last], (x[last].double() @ w[1].double().t()).to(torch.bfloat16))
+    dy = ints(3, rows, 64, hi=1)
+    dw = md.md_expert_wgrad(dy, x, off, cnt)
+    assert torch.equal(dw[1].double(), dy[last].double().t() @ x[last].double())
+    out = md.md_expert_gemm(dy, w, off, cnt, md.MD_W_KN, out=x)  # [rows, 8192] out
+    assert torch.equal(out[last], (dy[last].double() @ w[1].double()).to(torch.bfloat16))
+
+
+def test_far_experts_of_w_and_dw():
+    E, N, K, c = 257, 4096, 2056, 3  # 2.2e9 weights
+    counts = [0] * E
+    counts[E - 1] = c
+    off, cnt, rows, spans = groups(counts)
+    w = torch.zeros(E, N, K, dtype=torch.bfloat16, device=DEV)
+    w[E - 1] = ints(1, N, K, hi=1)
+    x = ints(2, rows, K, hi=1)
+    y = md.md_expert_gemm(x, w, off, cnt)
+    assert torch.equal(y, (x.double() @ w[E - 1].double().t()).to(torch.bfloat16))
+    dw = md.md_expert_wgrad(y, x, off, cnt, dw=w)  # bf16
+    assert torch.equal(dw[E - 1], (y.double().t() @ x.double()).to(torch.bfloat16))
+    assert not bool(dw[:E - 1].any())
+
+
+def test_far_rows_of_the_checkpoint():
+    rows, F, K, c = 140000, 8192, 64, 70
+    off, cnt = _far(rows, [c, c])
+    last = slice(rows - c, rows)
+    x, w = ints(1, rows, K, hi=1), ints(2, 2, 2 * F, K, hi=1)
+    act, codes, scales = md.md_expert_gated(x, w, off, cnt, keep=True)  # 2.3e9 codes
+    h = x[last].double() @ w[1].double().t()
+    want = h[:, :F] * torch.sigmoid(h[:, :F]) * h[:, F:]
+    assert bool(((act[last].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -20) * want.abs() + 1e-37).all())
+    g, u = restore64(codes[last], scales[last], F)
+    assert torch.equal(g, stored64(h[:, :F])[0]) and torch.equal(u, stored64(h[:, F:])[0])
+    codes[:rows - c].zero_()
+    scales[:rows - c].zero_()
+    da = torch.zeros(rows, F, dtype=torch.bfloat16, device=DEV)
+    da[last] = randn(3, c, F)
+    dh, again = md.md_expert_gated_backward(da, codes, scales)
+    near = md.md_expert_gated_backward(da[last].contiguous(), codes[last].contiguous(), scales[last].contiguous())
+    assert torch.equal(dh[last], near[0]) and torch.equal(again[last], near[1])
+
+
+def test_far_rows_of_combine_backward():
+    T, H, rows = 40, 8192, 270000
+    dout = randn(1, T, H)
+    y = torch.zeros(rows, H, dtype=torch.bfloat16, device=DEV)
+    at = torch.arange(rows - 2 * T, rows, dtype=torch.int32, device=DEV).flip(0).view(T, 2).contiguous()
+    y[rows - 2 * T:] = randn(2, 2 * T, H)
+    w = torch.rand(T, 2, device=DEV)
+    dy, dw = md.md_combine_backward(dout, at, w, y)
+    near = md.md_combine_backward(dout, (at - (rows - 2 * T)).contiguous(), w, y[rows - 2 * T:].contiguous())
+    assert torch.equal(dy[rows - 2 * T:], near[0]) and torch.equal(dw, near[1])
+
+
 @pytest.mark.parametrize("layout", [md.MD_W_NK, md.MD_W_KN])
 @pytest.mark.parametrize("counts,K,N", [([7, 0, 33], 128, 136), ([260, 31, 0, 512], 320, 264)])
 def test_gemm_is_exact_on_small_integers_and_leaves_other_rows(counts, K, N, layout):
