@@ -38,7 +38,7 @@ constexpr int kABytes = kTileM * kTileK * 2;
 constexpr int kBlock = 32;   // columns that share a scale of the 8-bit checkpoint
 constexpr int kMaxSplit = 4; // CTAs that share a contraction (few rows)
 constexpr long long kPolls = 1ll << 22;
-constexpr long long kDrainPolls = 1ll << 20;
+constexpr long long kDrainPolls = 1ll << 14;  // each may sleep for some microseconds
 
 // Division by a number fixed at launch: exact for 0 <= x < 2^31 (d >= 1), by the
 // round-up reciprocal of Granlund and Montgomery, with x below 2^31 in 33 bits.
@@ -429,8 +429,9 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
     md::tmem_fence_after();
     const uint32_t tmem = sh->tmem;
 
-    const int total = sh->tiles * (int)a.mt.d;  // the host keeps it below 2^30
     const int first = blockIdx.x / a.split, step = gridDim.x / a.split;
+    int total = sh->tiles * (int)a.mt.d;  // the host keeps it below 2^30
+    if (a.split > 1) total = min(total, step);  // one tile to a cluster, even if ranges overlap
     const uint32_t sbase = md::smem_addr(base);
     // blocks of the contraction: [kb0, kb1) in this CTA
     const int kblocks = (a.k + kTileK - 1) / kTileK;
@@ -603,6 +604,8 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
 // results are therefore summed in TMEM over kSegment blocks at most, in equal shares, and
 // then added in dw, in order: 0.9e-6, for 5% of the time.  (32 blocks: 1.1e-6.)
 constexpr int kSegment = 18;
+
+constexpr int kLaunchRegisters = 168;  // 12 warps of them: the sum of the split 8 x 216 + 4 x 72
 
 template <int MODE>
 struct Wide {
@@ -1037,14 +1040,18 @@ if (blocks == 0) {  // an expert without rows
 
 // ------------------------------------------------------------------ host
 
-// One launch in clusters of `members` CTAs.
+// One launch in clusters of `members` CTAs of a kernel that needs `registers` a thread.
 template <class Kernel, class... Params>
-int launch(Kernel kernel, int threads, size_t smem, size_t most_smem, std::atomic<uint64_t> &setup, int64_t clusters,
+int launch(Kernel kernel, int threads, int registers, size_t smem, size_t most_smem, std::atomic<uint64_t> &setup, int64_t clusters,
            int members, cudaStream_t s, const Params &...params)
 {
     md::once_per_device(setup, [&] {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem) != cudaSuccess)
-            cudaGetLastError();  // the launch then fails and reports MD_ERR_CUDA
+        // the wide form's register split draws on what the block is launched with: fewer registers
+        // than the split's sum would never be granted, so such a build is not launched
+        cudaFuncAttributes at = {};
+        const bool enough = cudaFuncGetAttributes(&at, kernel) == cudaSuccess && at.numRegs >= registers;
+        if (!enough || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem) != cudaSuccess)
+            cudaGetLastError();  // without its shared memory the launch fails and reports MD_ERR_CUDA
     });
     const int64_t most = md::sm_count() / members;
     cudaLaunchConfig_t cfg = {};
@@ -1103,7 +1110,7 @@ int run_few(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int
     while (a.split < kMaxSplit && tiles * a.split * 2 <= md::sm_count() && a.k >= a.split * 2 * 4 * kTileK)
         a.split *= 2;
     static std::atomic<uint64_t> setup{0};
-    return launch(k_expert_few<MODE>, P::kThreads, P::smem(a.E), P::smem(MD_MAX_EXPERTS), setup, tiles, a.split, s, ma,
+    return launch(k_expert_few<MODE>, P::kThreads, 0, P::smem(a.E), P::smem(MD_MAX_EXPERTS), setup, tiles, a.split, s, ma,
                   mb, a);
 }
 
@@ -1130,7 +1137,7 @@ int run_wide(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, in
     a.mt = FastDiv((uint32_t)mt);
     if (row_tiles * mt > kMostTiles) return MD_ERR_UNSUPPORTED;
     static std::atomic<uint64_t> setup{0};
-    return launch(k_expert_wide<MODE>, W::kThreads, W::smem(a.E), W::smem(MD_MAX_EXPERTS), setup, row_tiles * mt, 2, s, ma,
+    return launch(k_expert_wide<MODE>, W::kThreads, kLaunchRegisters, W::smem(a.E), W::smem(MD_MAX_EXPERTS), setup, row_tiles * mt, 2, s, ma,
                   mb, mb, a);
 }
 
@@ -1251,6 +1258,6 @@ extern "C" int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int 
     a.mt = FastDiv((uint32_t)mt);
     a.per = FastDiv((uint32_t)(mt * across));
     static std::atomic<uint64_t> setup{0};
-    return launch(k_expert_wide<kWgrad>, W::kThreads, W::smem(E), W::smem(MD_MAX_EXPERTS), setup, tiles, 2, s, ma, mb,
+    return launch(k_expert_wide<kWgrad>, W::kThreads, kLaunchRegisters, W::smem(E), W::smem(MD_MAX_EXPERTS), setup, tiles, 2, s, ma, mb,
                   mo, a);
 }

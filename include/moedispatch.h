@@ -710,6 +710,8 @@ int md_expert_gated(const void *x, int64_t rows, int K, const void *w, int E, in
  *   dw  [E, N, K], float32 (MD_F32) or bf16 (MD_BF16)
  *   accumulate  1: added to dw (MD_F32 only); 0: dw is overwritten, with
  *               zeros for experts without rows
+ * float32 results are summed in parts of at most 1152 rows, which are then
+ * added in float32 in their order: the same bits at every call.
  * For weights in MD_W_KN order pass x and dy in each other's place.
  */
 int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int E, int N, int K,
@@ -743,7 +745,8 @@ int md_expert_gated_backward(const void *da, const void *codes, const uint8_t *s
  *   dw          float32 [T, k]       out, or NULL: sum_h dout[t][h] y[row][h],
  *                                    summed in float32 in a fixed order
  * A row index outside [0, y_rows) is skipped and reported (MD_ERR_DATA), its
- * dw is 0.  dy must not overlap y or dout.
+ * dw is 0.  No row is named twice (as in a layout); dy must not overlap y or
+ * dout.
  */
 int md_combine_backward(const void *dout, const void *y, int64_t y_rows, const int32_t *assign_row,
                         const float *topk_w, int64_t T, int k, int H, void *dy, float *dw,

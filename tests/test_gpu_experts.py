@@ -807,3 +807,55 @@ def test_a_wait_that_runs_out_is_reported_and_leaves_the_gpu_usable():
     md.check_status(st)
     want, _ = products64(x, w, spans)
     assert torch.equal(y, want.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("form", ["wide", "wide gated", "shared"])
+def test_a_wait_that_runs_out_in_each_form(form):
+    """The same in the pairs' kernel and where CTAs share a contraction."""
+    from combine_warp_top_router_b200 import binding
+    counts, K, N = ([2], 2048, 264) if form == "shared" else ([300] * 40, 512, 528)
+    off, cnt, rows, spans = groups(counts)
+    x, w = ints(1, rows, K, hi=1), ints(2, len(counts), N, K, hi=1)
+
+    def call(st):
+        if form == "wide gated":
+            return md.md_expert_gated(x, w, off, cnt, keep=True, dev_status=st)
+        return md.md_expert_gemm(x, w, off, cnt, dev_status=st)
+
+    st = md.new_status(DEV)
+    binding.lib().md_set_test_hooks(1, -1, -1)
+    try:
+        call(st)
+        assert int(st.item()) == md.MD_ERR_TIMEOUT
+    finally:
+        binding.lib().md_set_test_hooks(0, -1, -1)
+    first, again = call(st), call(st)
+    md.check_status(st)
+    for a, b in zip(first, again):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    if form != "wide gated":
+        want, _ = products64(x, w, spans)
+        assert torch.equal(first, want.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("op", ["gemm", "gated", "wgrad"])
+def test_first_call_may_be_captured(op):
+    """A call whose shapes no warm-up has seen, captured at once and replayed on new inputs."""
+    counts, K, N = [70, 0, 300, 5], 200, 144
+    off, cnt, rows, spans = groups(counts)
+    x, w, dy = ints(1, rows, K, hi=1), ints(2, 4, N, K, hi=1), ints(3, rows, N, hi=1)
+    call = {"gemm": lambda: md.md_expert_gemm(x, w, off, cnt),
+            "gated": lambda: md.md_expert_gated(x, w, off, cnt, keep=True)[1].view(torch.uint8),
+            "wgrad": lambda: md.md_expert_wgrad(dy, x, off, cnt)}[op]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    # other rows, another split of them among the experts
+    x.copy_(ints(7, rows, K, hi=1))
+    off2, cnt2, _, _ = groups([5, 300, 0, 70], seed=3)
+    off.copy_(off2)
+    cnt.copy_(cnt2)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, call())
