@@ -960,10 +960,9 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
             for (int i = 0; i < 4; ++i) read(v[i], i);
             give_back();
         };
-        // the subs' accumulators, out through put(values, sub, run).  Sub 1's is taken as soon as
-        // put's own registers allow: a spilled value would come back from L2, under all that
-        // traffic some 1500 cycles a load.
-        constexpr int kBefore = MODE == kGated ? 3 : 2;
+        // the subs' accumulators, out through put(values, sub, run).  Sub 1's is taken when half of sub
+        // 0's is out, as soon as the registers allow (one run later: 1 to 4% slower).
+        constexpr int kBefore = 2;
         auto results = [&](int subs, auto put) __attribute__((always_inline)) {
             uint32_t v[4][32];
             take(v);
