@@ -6,7 +6,9 @@ profiling a single kernel under ncu on a small case.
 
 Steps: topk, layout, permute, combine, wire, expand, coselect, place, shuffle, shuffle_rounds,
 shuffle_pair (three_layer_e128_k6 only), gather, exchange (the EP exchange with every rank on
-this GPU: R dispatch-exchange calls, R partials calls, R combine-exchange calls).
+this GPU: R dispatch-exchange calls, R partials calls, R combine-exchange calls), experts (the
+gated up- and the down-projection on the expert-grouped rows), experts_backward (the gradients
+back from the combine's output; F inner columns, --F).
 Every listed step runs once as warm-up and then `reps` times.
 """
 from __future__ import annotations
@@ -26,12 +28,14 @@ def main():
     ap.add_argument("--T", type=int, default=None)
     ap.add_argument("--H", type=int, default=None)
     ap.add_argument("--R", type=int, default=None)
+    ap.add_argument("--F", type=int, default=1024)
     ap.add_argument("--mode", choices=["dedup", "conv"], default="dedup")
     ap.add_argument("--reps", type=int, default=3)
     a = ap.parse_args()
     steps = a.steps.split(",")
     dev = torch.device("cuda", 0)
-    rows = any(s in steps for s in ("permute", "combine", "wire", "expand", "gather", "exchange"))
+    rows = any(s in steps for s in ("permute", "combine", "wire", "expand", "gather", "exchange",
+                                   "experts", "experts_backward"))
     w = synth.make_workload(a.workload, device=dev, T=a.T, H=a.H, R=a.R, with_rows=rows)
     mode = md.MD_DEDUP if a.mode == "dedup" else md.MD_CONV
     T, E, k, R = w.T, w.E, w.k, w.R
@@ -51,6 +55,8 @@ def main():
         idx0, _ = md.md_route_topk(w.logits_prev, k)
         C2 = md.md_coselect_pair_stats(idx0, idx, idx2, E, T_fit=w.fit_tokens or T)
     ex = _exchange_setup(w, idx, gates, dev) if "exchange" in steps else None
+    experts = [s for s in steps if s.startswith("experts")]
+    moe = _experts_setup(w, L, idx, gates, a.F) if experts else None
     torch.cuda.synchronize()
 
     def once():
@@ -82,6 +88,10 @@ def main():
                 md.md_gather_rows(w.x, torch.arange(T, dtype=torch.int32, device=dev).flip(0))
             elif s == "exchange":
                 _exchange_run(w, idx, gates, ex)
+            elif s == "experts":
+                _experts_forward(moe)
+            elif s == "experts_backward":
+                _experts_backward(moe)
             else:
                 raise SystemExit(f"unknown step {s}")
 
@@ -89,6 +99,37 @@ def main():
         once()
     torch.cuda.synchronize()
     print("ok", a.workload, "T", T, "steps", steps, "reps", a.reps)
+
+
+def _experts_setup(w, L, idx, gates, F):
+    """The dispatched rows in expert order, random weights of an expert layer with F inner
+    columns, and what its forward pass keeps."""
+    dev, H, E = w.x.device, w.H, w.E
+    g = torch.Generator(device=dev).manual_seed(11)
+
+    def normal(*shape):
+        return (torch.randn(*shape, generator=g, device=dev) * shape[-1] ** -0.5).to(torch.bfloat16)
+
+    m = dict(x=md.md_dispatch_permute(w.x, L.assign_row), w13=normal(E, 2 * F, H), w2=normal(E, H, F),
+             dout=normal(w.T, H), L=L, gates=gates)
+    _experts_forward(m)
+    return m
+
+
+def _experts_forward(m):
+    span = (m["L"].expert_offsets, m["L"].expert_counts)
+    m["act"], m["codes"], m["scales"] = md.md_expert_gated(m["x"], m["w13"], *span, keep=True)
+    m["y"] = md.md_expert_gemm(m["act"], m["w2"], *span)
+
+
+def _experts_backward(m):
+    span = (m["L"].expert_offsets, m["L"].expert_counts)
+    dy, _ = md.md_combine_backward(m["dout"], m["L"].assign_row, m["gates"], m["y"])
+    da = md.md_expert_gemm(dy, m["w2"], *span, md.MD_W_KN)
+    dh, act = md.md_expert_gated_backward(da, m["codes"], m["scales"])
+    md.md_expert_wgrad(dy, act, *span)
+    md.md_expert_wgrad(dh, m["x"], *span)
+    md.md_expert_gemm(dh, m["w13"], *span, md.MD_W_KN)
 
 
 def _exchange_setup(w, idx, gates, dev):
