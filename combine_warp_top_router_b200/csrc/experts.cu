@@ -261,34 +261,39 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
 // Eight columns of one row and one half of the checkpoint.  The four lanes of
 // a 32-column block share its scale: the smallest 2^s with amax <= 448 * 2^s.
 // 448 = 1.75 * 2^8, so s follows from amax's exponent and whether its fraction
-// passes 1.75.  Inf and NaN are left out of amax and stored as NaN.
+// passes 1.75.  Inf and NaN are left out of amax and stored as NaN: a maximum drops
+// NaN by itself and the conversion keeps it; blocks with Inf (or nothing but NaN)
+// are looked through again.
 __device__ __forceinline__ void pack_block(const float (&v)[8], bool valid, bool store, uint8_t *code,
                                            uint8_t *scale, bool owner)
 {
-    uint32_t m = 0;
+    auto of_block = [](float m) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    };
+    float m = fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
+                    fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
+    m = of_block(valid ? m : 0.0f);
+    const bool odd = __any_sync(0xffffffffu, !(m < INFINITY));
+    if (odd) {
+        float f = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
-        if (u < 0x7f800000u && valid) m = m > u ? m : u;
+        for (int i = 0; i < 8; ++i) f = fabsf(v[i]) < INFINITY && valid ? fmaxf(f, fabsf(v[i])) : f;
+        m = of_block(f);
     }
-    uint32_t o = __shfl_xor_sync(0xffffffffu, m, 1);
-    m = m > o ? m : o;
-    o = __shfl_xor_sync(0xffffffffu, m, 2);
-    m = m > o ? m : o;
-    int s = (int)(m >> 23) - 8 + ((m & 0x7fffffu) > 0x600000u ? 1 : 0);
+    const uint32_t bits = __float_as_uint(m);
+    int s = (int)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
     s = s < 0 ? 0 : s;  // biased by 127
     if (!store) return;
     const float inv = __uint_as_float((uint32_t)(254 - s) << 23);  // 2^(127 - s), s <= 247
     uint32_t w[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float q[4];
+    for (int h = 0; h < 2; ++h)
+        w[h] = e4m3x2(v[4 * h] * inv, v[4 * h + 1] * inv) | (e4m3x2(v[4 * h + 2] * inv, v[4 * h + 3] * inv) << 16);
+    if (odd) {  // the conversion would keep Inf as 448
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float x = v[4 * h + i];
-            q[i] = (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : x * inv;
-        }
-        w[h] = e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(v[i]) == INFINITY) w[i >> 2] |= 0x7fu << (i & 3) * 8;
     }
     *reinterpret_cast<uint2 *>(code) = make_uint2(w[0], w[1]);
     if (owner) *scale = (uint8_t)s;
@@ -337,23 +342,24 @@ __device__ __forceinline__ void emit(const uint32_t (&v)[32], int c, const Tile 
             const int ii = in ? i0 + (lane >> 3) : i0;
             float g[8], u[8];
             const float *at = st + (ii - h) * kTileM + j * 8;
+            const int64_t r = q.r0 + c + ii;
+            const int blocks = (a.n + kBlock - 1) / kBlock;
             *reinterpret_cast<float4 *>(g) = *reinterpret_cast<const float4 *>(at);
             *reinterpret_cast<float4 *>(g + 4) = *reinterpret_cast<const float4 *>(at + 4);
+            if (a.codes)
+                pack_block(g, valid, valid && in, a.codes + r * 2 * a.n + f0, a.scales + r * 2 * blocks + f0 / kBlock,
+                           (j & 3) == 0);
+#pragma unroll
+            for (int p = 0; p < 8; ++p) g[p] *= md::sigmoid(g[p]);
             *reinterpret_cast<float4 *>(u) = *reinterpret_cast<const float4 *>(at + 64);
             *reinterpret_cast<float4 *>(u + 4) = *reinterpret_cast<const float4 *>(at + 68);
-            const int64_t r = q.r0 + c + ii;
-            if (a.codes) {
-                const int blocks = (a.n + kBlock - 1) / kBlock;
-                uint8_t *cr = a.codes + r * 2 * a.n + f0, *sr = a.scales + r * 2 * blocks + f0 / kBlock;
-                pack_block(g, valid, valid && in, cr, sr, (j & 3) == 0);
-                pack_block(u, valid, valid && in, cr + a.n, sr + blocks, (j & 3) == 0);
-            }
+            if (a.codes)
+                pack_block(u, valid, valid && in, a.codes + r * 2 * a.n + a.n + f0,
+                           a.scales + r * 2 * blocks + blocks + f0 / kBlock, (j & 3) == 0);
             if (valid && in) {
                 uint32_t w[4];
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    w[p] = md::pack_bf16x2(g[2 * p] * md::sigmoid(g[2 * p]) * u[2 * p],
-                                           g[2 * p + 1] * md::sigmoid(g[2 * p + 1]) * u[2 * p + 1]);
+                for (int p = 0; p < 4; ++p) w[p] = md::pack_bf16x2(g[2 * p] * u[2 * p], g[2 * p + 1] * u[2 * p + 1]);
                 *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + r * a.pitch + f0) =
                     make_uint4(w[0], w[1], w[2], w[3]);
             }
