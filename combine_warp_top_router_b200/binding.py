@@ -752,7 +752,7 @@ def md_expert_gated_backward(da, codes, scales, dh=None, act=None, want_act=True
     if act is not None:
         _exact(act, "act", torch.bfloat16, dev, (rows, F))
     elif want_act:
-        act = da.new_empty((rows, F))
+        act = torch.empty_like(da)
     _, stream = _tail(None, stream, dev)
     rc = _call("md_expert_gated_backward", dev, da.data_ptr(), codes.data_ptr(), scales.data_ptr(), rows,
                F, dh.data_ptr(), None if act is None else act.data_ptr(), stream)
@@ -777,12 +777,14 @@ def md_combine_backward(dout, assign_row, topk_w, y=None, y_rows=None, dy=None, 
         y_rows = y.shape[0]
         _exact(y, "y", torch.bfloat16, dev, (y_rows, H))
         if dw is None:
-            dw = topk_w.new_empty((T, k))
+            dw = torch.empty_like(topk_w)
         else:
             _exact(dw, "dw", torch.float32, dev, (T, k))
     elif dw is not None:
         raise ValueError("dw needs y (the expert outputs)")
-    if dy is None:
+    if dy is None and y is not None:
+        dy = torch.empty_like(y)
+    elif dy is None:
         dy = dout.new_empty((T * k if y_rows is None else y_rows, H))
     else:
         _exact(dy, "dy", torch.bfloat16, dev, (dy.shape[0] if y_rows is None else y_rows, H))

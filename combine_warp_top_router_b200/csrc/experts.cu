@@ -37,7 +37,7 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kLoadXWarp = 10;
 constexpr int kABytes = kTileM * kTileK * 2;
 constexpr int kBlock = 32;   // columns that share a scale of the 8-bit checkpoint
 constexpr int kMaxSplit = 4; // CTAs that share a contraction (few rows)
-constexpr long long kPolls = 1ll << 22;
+constexpr long long kWaitCycles = 1ll << 32;  // a wait's limit while its CTA loads nothing: some two seconds
 constexpr long long kDrainPolls = 1ll << 14;  // each may sleep for some microseconds
 
 // Division by a number fixed at launch: exact for 0 <= x < 2^31 (d >= 1), by the
@@ -72,30 +72,49 @@ struct Args {
     FastDiv per;  // wgrad: tiles of an expert
     int split;    // k_expert_few: CTAs (a cluster) that share each tile's contraction; each cluster has one tile
     int32_t *status;
-    long long polls;
+    long long polls;  // a wait's looks at most (test hook)
 };
 
 // What the roles of a CTA share, besides their barriers.
 struct Shared {
     uint32_t tmem;
     int abort;
+    unsigned loads;  // counts up as the loading warp goes on: a sign of life for the other roles' waits
     int tiles;  // ragged row tiles of all experts
 };
 
 // Bounded wait of a converged warp; all lanes get the same answer.  The first look
-// does not sleep, the others may.  On run-out raises the CTA's abort flag.
+// does not sleep, the others may.  A wait may be as long as its tile, so the limit
+// is on the time without a load; on run-out the CTA's abort flag is raised.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Shared *sh, const Args &a)
 {
     if (__all_sync(0xffffffffu, md::mbar_test_wait(bar, parity))) return true;
     volatile int *ab = &sh->abort;
+    volatile unsigned *loads = &sh->loads;
+    long long since = clock64();
+    unsigned seen = *loads;
     for (long long i = 1; i < a.polls; ++i) {
         if (__any_sync(0xffffffffu, *ab)) return false;
         if (__all_sync(0xffffffffu, md::mbar_try_wait(bar, parity))) return true;
+        const unsigned now = *loads;
+        if (__any_sync(0xffffffffu, now != seen)) {
+            seen = now;
+            since = clock64();
+        } else if (__any_sync(0xffffffffu, clock64() - since > kWaitCycles)) {
+            break;
+        }
     }
     *ab = 1;
     if ((threadIdx.x & 31) == 0) md::report(a.status, MD_ERR_TIMEOUT);
     __syncwarp();
     return false;
+}
+
+// By the loading warp, every 64 blocks of a tile.
+__device__ __forceinline__ void sign_of_life(Shared *sh, unsigned n)
+{
+    if ((threadIdx.x & 31) == 0) *(volatile unsigned *)&sh->loads = n;
+    __syncwarp();
 }
 
 // Wait of the epilogue's warps: the first polls, the others sleep at a barrier,
@@ -420,6 +439,7 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
         }
         md::mbar_init(&b->drain, 1);
         sh->abort = 0;
+        sh->loads = 0;
         md::fence_mbar_init();
     }
     if (warp == kLoadWarp && lane == 0) {
@@ -451,71 +471,69 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------ loads
-        {
-            Turn at(P::kStages);
-            int used = 0;  // stages loaded at least once
-            bool ok = true;
-            for (int t = first; ok && t < total; t += step) {
-                const Tile q = tile_of(t);
-                const int boxes = (q.n + P::kBox - 1) / P::kBox, r0 = (int)q.r0;
-                const uint32_t bytes = kABytes + boxes * P::kBox * 128;
-                for (int i = kb0; i < kb1; ++i) {
-                    const int s = at.s;
-                    if (!(ok = warp_wait(&b->empty[s], at.parity ^ 1u, sh, a))) break;
-                    const uint32_t bar = md::smem_addr(&b->full[s]);
-                    md::expect_tx_one(&b->full[s], bytes);
-                    const uint32_t sa = sbase + s * P::kStageBytes, sb = sa + kABytes;
-                    const int k0 = i * kTileK;
-                    if (MODE == kNK) {
-                        md::tma_load_3d<1>(sa, &map_a, k0, q.m0, q.e, bar);
-                    } else if (MODE == kGated) {
-                        md::tma_load_3d<1>(sa, &map_a, k0, q.m0, q.e, bar);
-                        md::tma_load_3d<1>(sa + 8192, &map_a, k0, a.n + q.m0, q.e, bar);
-                    } else {
-                        md::tma_load_3d<1>(sa, &map_a, q.m0, k0, q.e, bar);
-                        md::tma_load_3d<1>(sa + 8192, &map_a, q.m0 + 64, k0, q.e, bar);
-                    }
-                    for (int j = 0; j < boxes; ++j)
-                        md::tma_load_2d<1>(sb + j * P::kBox * 128, &map_b, k0, r0 + j * P::kBox, bar);
-                    if (used < P::kStages) ++used;
-                    at.next();
+        Turn at(P::kStages);
+        int used = 0;         // stages loaded at least once
+            unsigned begun = 0;  // signs of life
+        bool ok = true;
+        for (int t = first; ok && t < total; t += step) {
+            const Tile q = tile_of(t);
+            const int boxes = (q.n + P::kBox - 1) / P::kBox, r0 = (int)q.r0;
+            const uint32_t bytes = kABytes + boxes * P::kBox * 128;
+            for (int i = kb0; i < kb1; ++i) {
+                const int s = at.s;
+                if (!(ok = warp_wait(&b->empty[s], at.parity ^ 1u, sh, a))) break;
+                const uint32_t bar = md::smem_addr(&b->full[s]);
+                if (i % 64 == 0) sign_of_life(sh, ++begun);
+                md::expect_tx_one(&b->full[s], bytes);
+                const uint32_t sa = sbase + s * P::kStageBytes, sb = sa + kABytes;
+                const int k0 = i * kTileK;
+                if (MODE == kNK) {
+                    md::tma_load_3d<1>(sa, &map_a, k0, q.m0, q.e, bar);
+                } else if (MODE == kGated) {
+                    md::tma_load_3d<1>(sa, &map_a, k0, q.m0, q.e, bar);
+                    md::tma_load_3d<1>(sa + 8192, &map_a, k0, a.n + q.m0, q.e, bar);
+                } else {
+                    md::tma_load_3d<1>(sa, &map_a, q.m0, k0, q.e, bar);
+                    md::tma_load_3d<1>(sa + 8192, &map_a, q.m0 + 64, k0, q.e, bar);
                 }
+                for (int j = 0; j < boxes; ++j)
+                    md::tma_load_2d<1>(sb + j * P::kBox * 128, &map_b, k0, r0 + j * P::kBox, bar);
+                if (used < P::kStages) ++used;
+                at.next();
             }
-            drain_loads(at, used, b->full);
         }
+        drain_loads(at, used, b->full);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------ products
-        {
-            constexpr bool kAKMajor = MODE != kKN;
-            const uint64_t da0 = kAKMajor ? md::operand_desc(sbase, 16, 1024) : md::operand_desc(sbase, 8192, 1024);
-            const uint64_t db0 = md::operand_desc(sbase + kABytes, 16, 1024);
-            constexpr int kAStep = (kAKMajor ? 32 : 2048) >> 4;
-            Turn at(P::kStages);
-            int acc = 0;
-            bool ok = true;
-            for (int t = first; ok && t < total; t += step, ++acc) {
-                const Tile q = tile_of(t);
-                const int buf = acc & 1;
-                const uint32_t idesc = md::mma_desc(kTileM, q.n, !kAKMajor, false), d = tmem + buf * BN;
-                if (!warp_wait(&b->tempty[buf], (uint32_t)((acc >> 1) & 1) ^ 1u, sh, a)) break;
+        constexpr bool kAKMajor = MODE != kKN;
+        const uint64_t da0 = kAKMajor ? md::operand_desc(sbase, 16, 1024) : md::operand_desc(sbase, 8192, 1024);
+        const uint64_t db0 = md::operand_desc(sbase + kABytes, 16, 1024);
+        constexpr int kAStep = (kAKMajor ? 32 : 2048) >> 4;
+        Turn at(P::kStages);
+        int acc = 0;
+        bool ok = true;
+        for (int t = first; ok && t < total; t += step, ++acc) {
+            const Tile q = tile_of(t);
+            const int buf = acc & 1;
+            const uint32_t idesc = md::mma_desc(kTileM, q.n, !kAKMajor, false), d = tmem + buf * BN;
+            if (!warp_wait(&b->tempty[buf], (uint32_t)((acc >> 1) & 1) ^ 1u, sh, a)) break;
+            md::tmem_fence_after();
+            for (int i = kb0; i < kb1; ++i) {
+                const int s = at.s;
+                if (!(ok = warp_wait(&b->full[s], at.parity, sh, a))) break;
                 md::tmem_fence_after();
-                for (int i = kb0; i < kb1; ++i) {
-                    const int s = at.s;
-                    if (!(ok = warp_wait(&b->full[s], at.parity, sh, a))) break;
-                    md::tmem_fence_after();
-                    const uint64_t da = da0 + (uint32_t)(s * (P::kStageBytes >> 4));
-                    const uint64_t db = db0 + (uint32_t)(s * (P::kStageBytes >> 4));
+                const uint64_t da = da0 + (uint32_t)(s * (P::kStageBytes >> 4));
+                const uint64_t db = db0 + (uint32_t)(s * (P::kStageBytes >> 4));
 #pragma unroll
-                    for (int j = 0; j < kTileK / 16; ++j)
-                        md::mma_bf16<1>(d, da + j * kAStep, db + j * 2, idesc, i > kb0 || j > 0);
-                    md::mma_commit<1>(&b->empty[s]);
-                    if (i == kb1 - 1) md::mma_commit<1>(&b->tfull[buf]);
-                    at.next();
-                }
+                for (int j = 0; j < kTileK / 16; ++j)
+                    md::mma_bf16<1>(d, da + j * kAStep, db + j * 2, idesc, i > kb0 || j > 0);
+                md::mma_commit<1>(&b->empty[s]);
+                if (i == kb1 - 1) md::mma_commit<1>(&b->tfull[buf]);
+                at.next();
             }
-            md::mma_commit<1>(&b->drain);  // await the MMAs in flight, whoever gave up
-            md::mbar_wait_bounded(&b->drain, 0, kDrainPolls);
         }
+        md::mma_commit<1>(&b->drain);  // await the MMAs in flight, whoever gave up
+        md::mbar_wait_bounded(&b->drain, 0, kDrainPolls);
     } else {
         // ------------------------------------------------ results
         int acc = 0;
@@ -711,6 +729,7 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
         }
         md::mbar_init(&b->drain, 1);
         sh->abort = 0;
+        sh->loads = 0;
         md::fence_mbar_init();
     }
     if (warp == kLoadWarp && lane == 0) md::prefetch_map(&map_a);
@@ -768,69 +787,69 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kLoadWarp || warp == kLoadXWarp) {
             // ------------------------------------------------ loads
-            {
-                Turn at(stages);
-                int used = 0;  // stages loaded at least once
-                uint32_t tails = 0, used_tails = 0;
-                bool ok = true;
-                for (int round = 0; ok && round < rounds; ++round) {
-                    const int t = deal(round);
-                    if (t >= total) continue;
-                    const Tile q = tile_of(t);
-                    const int subs = q.subs, kb = blocks_of(q);
-                    const int half = q.n / 2, boxes = (half + 63) / 64;  // N-side lines of this CTA
-                    const int r0 = (int)q.r0 + (kWg ? 0 : rank * half), c0 = q.c0 + rank * half;
-                    const uint32_t bytes = warp == kLoadWarp ? subs * W::kPart : boxes * 8192;
-                    for (int i = 0; i < kb; ++i) {
-                        if (!(ok = warp_wait(&b->empty[at.s], at.parity ^ 1u, sh, a))) break;
-                        // the first CTA's barrier counts both CTAs' bytes, but for a block to be cleared
-                        const bool tail = kWg && i == kb - 1 && q.count % kTileK != 0;
-                        uint32_t bar = md::map_rank(md::smem_addr(&b->full[at.s]), 0);
-                        if (rank == 0) {
-                            md::expect_tx_one(&b->full[at.s], tail ? bytes : 2 * bytes);
-                        } else if (tail) {
-                            md::expect_tx_one(&b->tail[at.s], bytes);
-                            bar = md::map_rank(md::smem_addr(&b->tail[at.s]), 1);
-                            used_tails |= 1u << at.s;
-                            tails ^= 1u << at.s;
-                        }
-                        const uint32_t to = sbase + at.s * stage_bytes;
-                        const int k0 = i * kTileK;
-                        if (warp == kLoadXWarp) {
-                            for (int j = 0; j < boxes; ++j) {
-                                const uint32_t tx = to + W::kPart + j * 8192;
-                                if (kWg) md::tma_load_2d<2>(tx, &map_b, c0 + j * 64, r0 + k0, bar);
-                                else md::tma_load_2d<2>(tx, &map_b, k0, r0 + j * 64, bar);
-                            }
-                        } else {
-                            for (int sub = 0; sub < subs; ++sub) {
-                                const uint32_t ta = to + sub * 2 * W::kPart;
-                                const int m = q.m0 + sub * W::kSub;
-                                if (MODE == kNK) {
-                                    md::tma_load_3d<2>(ta, &map_a, k0, m, q.e, bar);
-                                } else if (MODE == kGated) {
-                                    md::tma_load_3d<2>(ta, &map_a, k0, m, q.e, bar);
-                                    md::tma_load_3d<2>(ta + 8192, &map_a, k0, a.n + m, q.e, bar);
-                                } else if (MODE == kKN) {
-                                    md::tma_load_3d<2>(ta, &map_a, m, k0, q.e, bar);
-                                    md::tma_load_3d<2>(ta + 8192, &map_a, m + 64, k0, q.e, bar);
-                                } else {
-                                    md::tma_load_2d<2>(ta, &map_a, m, r0 + k0, bar);
-                                    md::tma_load_2d<2>(ta + 8192, &map_a, m + 64, r0 + k0, bar);
-                                }
-                            }
-                        }
-                        if (used < stages) ++used;
-                        at.next();
+            Turn at(stages);
+            int used = 0;        // stages loaded at least once
+            unsigned begun = 0;  // signs of life
+            uint32_t tails = 0, used_tails = 0;
+            bool ok = true;
+            for (int round = 0; ok && round < rounds; ++round) {
+                const int t = deal(round);
+                if (t >= total) continue;
+                const Tile q = tile_of(t);
+                const int subs = q.subs, kb = blocks_of(q);
+                const int half = q.n / 2, boxes = (half + 63) / 64;  // N-side lines of this CTA
+                const int r0 = (int)q.r0 + (kWg ? 0 : rank * half), c0 = q.c0 + rank * half;
+                const uint32_t bytes = warp == kLoadWarp ? subs * W::kPart : boxes * 8192;
+                for (int i = 0; i < kb; ++i) {
+                    if (!(ok = warp_wait(&b->empty[at.s], at.parity ^ 1u, sh, a))) break;
+                    if (i % 64 == 0 && warp == kLoadWarp) sign_of_life(sh, ++begun);
+                    // the first CTA's barrier counts both CTAs' bytes, but for a block to be cleared
+                    const bool tail = kWg && i == kb - 1 && q.count % kTileK != 0;
+                    uint32_t bar = md::map_rank(md::smem_addr(&b->full[at.s]), 0);
+                    if (rank == 0) {
+                        md::expect_tx_one(&b->full[at.s], tail ? bytes : 2 * bytes);
+                    } else if (tail) {
+                        md::expect_tx_one(&b->tail[at.s], bytes);
+                        bar = md::map_rank(md::smem_addr(&b->tail[at.s]), 1);
+                        used_tails |= 1u << at.s;
+                        tails ^= 1u << at.s;
                     }
+                    const uint32_t to = sbase + at.s * stage_bytes;
+                    const int k0 = i * kTileK;
+                    if (warp == kLoadXWarp) {
+                        for (int j = 0; j < boxes; ++j) {
+                            const uint32_t tx = to + W::kPart + j * 8192;
+                            if (kWg) md::tma_load_2d<2>(tx, &map_b, c0 + j * 64, r0 + k0, bar);
+                            else md::tma_load_2d<2>(tx, &map_b, k0, r0 + j * 64, bar);
+                        }
+                    } else {
+                        for (int sub = 0; sub < subs; ++sub) {
+                            const uint32_t ta = to + sub * 2 * W::kPart;
+                            const int m = q.m0 + sub * W::kSub;
+                            if (MODE == kNK) {
+                                md::tma_load_3d<2>(ta, &map_a, k0, m, q.e, bar);
+                            } else if (MODE == kGated) {
+                                md::tma_load_3d<2>(ta, &map_a, k0, m, q.e, bar);
+                                md::tma_load_3d<2>(ta + 8192, &map_a, k0, a.n + m, q.e, bar);
+                            } else if (MODE == kKN) {
+                                md::tma_load_3d<2>(ta, &map_a, m, k0, q.e, bar);
+                                md::tma_load_3d<2>(ta + 8192, &map_a, m + 64, k0, q.e, bar);
+                            } else {
+                                md::tma_load_2d<2>(ta, &map_a, m, r0 + k0, bar);
+                                md::tma_load_2d<2>(ta + 8192, &map_a, m + 64, r0 + k0, bar);
+                            }
+                        }
+                    }
+                    if (used < stages) ++used;
+                    at.next();
                 }
-                if (rank == 0) drain_loads(at, used, b->full);
-                else
-                    for (int i = 0; i < stages; ++i)
-                        if (used_tails >> i & 1u) md::mbar_wait_bounded(&b->tail[i], (tails >> i & 1u) ^ 1u, kDrainPolls);
-                if (rank == 1 && !ok)
-                    for (int j = 0; j < 2000; ++j) __nanosleep(500);
             }
+            if (rank == 0) drain_loads(at, used, b->full);
+            else
+                for (int i = 0; i < stages; ++i)
+                    if (used_tails >> i & 1u) md::mbar_wait_bounded(&b->tail[i], (tails >> i & 1u) ^ 1u, kDrainPolls);
+            if (rank == 1 && !ok)
+                for (int j = 0; j < 2000; ++j) __nanosleep(500);
         } else if (warp == kMmaWarp) {
             // ------------------------------------------------ products
             // Clears the lines from v on, up to the last of `steps` sixteenths, of every box of a stage.
@@ -1014,7 +1033,7 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                         send_rows(&map_d, q.c0 + c - (odd ? 32 : 0), row0, q.e, add, st);
                         buffer ^= 4096;  // with each store made: a tile's edge may leave some out
                     };
-if (blocks == 0) {  // an expert without rows
+                    if (blocks == 0) {  // an expert without rows
                         uint32_t none[32] = {};
 #pragma unroll 1
                         for (int i = 0; i < 4 * subs; ++i) put(none, i >> 2, i & 3);
@@ -1182,7 +1201,7 @@ extern "C" int md_expert_gemm(const void *x, int64_t rows, int K, const void *w,
     a.pitch = N;
     a.y = y;
     a.status = dev_status;
-    a.polls = md::hook_poll_limit(kPolls);
+    a.polls = md::hook_poll_limit(INT64_MAX);
     if (w_layout == MD_W_NK)
         return few_rows(rows, E, N, Wide<kNK>::kSub) ? run_few<kNK>(x, w, rows, a, K, N, s)
                                                      : run_wide<kNK>(x, w, rows, a, K, N, s);
@@ -1215,7 +1234,7 @@ extern "C" int md_expert_gated(const void *x, int64_t rows, int K, const void *w
     a.codes = static_cast<uint8_t *>(codes);
     a.scales = scales;
     a.status = dev_status;
-    a.polls = md::hook_poll_limit(kPolls);
+    a.polls = md::hook_poll_limit(INT64_MAX);
     return few_rows(rows, E, F, Wide<kGated>::kSub) ? run_few<kGated>(x, w, rows, a, K, 2 * (int64_t)F, s)
                                                     : run_wide<kGated>(x, w, rows, a, K, 2 * (int64_t)F, s);
 }
@@ -1249,7 +1268,7 @@ extern "C" int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int 
     a.out_bf16 = out_type == MD_BF16;
     a.accumulate = accumulate != 0;
     a.status = dev_status;
-    a.polls = md::hook_poll_limit(kPolls);
+    a.polls = md::hook_poll_limit(INT64_MAX);
     a.y = dw;
     using W = Wide<kWgrad>;
     CUtensorMap ma, mb, mo;
