@@ -81,6 +81,7 @@ struct Shared {
     int abort;
     unsigned loads;  // counts up as the loading warp goes on: a sign of life for the other roles' waits
     int tiles;  // ragged row tiles of all experts
+    int sums[12];
 };
 
 // Bounded wait of a converged warp; all lanes get the same answer.  The first look
@@ -227,14 +228,14 @@ __device__ __forceinline__ void sort_experts(const Table &tab, const Args &a)
     __syncthreads();
 }
 
-// Exclusive running sum of the experts' row tiles, by one warp.
+// Exclusive running sum of the experts' row tiles, by all threads; barriers inside.
 template <int BN>
 __device__ __forceinline__ void count_tiles(const Table &tab, Shared *sh, const Args &a)
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     int run = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-        const int e = e0 + lane;
+    for (int e0 = 0; e0 < a.E; e0 += blockDim.x) {
+        const int e = e0 + threadIdx.x;
         const int own = e < a.E ? (tab.cnt(tab.order(e)) + BN - 1) / BN : 0;
         int v = own;
 #pragma unroll
@@ -242,23 +243,32 @@ __device__ __forceinline__ void count_tiles(const Table &tab, Shared *sh, const 
             const int o = __shfl_up_sync(0xffffffffu, v, d);
             if (lane >= d) v += o;
         }
-        if (e < a.E) tab.pre(e) = run + v - own;
-        run += __shfl_sync(0xffffffffu, v, 31);
+        if (lane == 31) sh->sums[warp] = v;
+        __syncthreads();
+        int before = run;
+        for (int w = 0; w < warps; ++w) {
+            before += w < warp ? sh->sums[w] : 0;
+            run += sh->sums[w];
+        }
+        if (e < a.E) tab.pre(e) = before + v - own;
+        __syncthreads();
     }
-    if (lane == 0) sh->tiles = run;
+    if (threadIdx.x == 0) sh->tiles = run;
 }
 
-// Rows of row tile rt.
+// Rows of row tile rt; a converged warp, which looks at 32 places of the order at once.
 template <int CG, int BN>
 __device__ __forceinline__ Tile rows_at(int rt, const Table &tab, const Args &a)
 {
     constexpr int kGran = 16 * CG;
-    int lo = 0, hi = a.E;  // last place in the order whose first tile is at or before rt
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (tab.pre(mid) <= rt) lo = mid;
-        else hi = mid;
-    }
+    // the last place in the order whose first tile is at or before rt: every `stride`-th first
+    const int lane = threadIdx.x & 31, stride = (a.E + 31) >> 5;
+    int at_place = lane * stride;
+    unsigned m = __ballot_sync(0xffffffffu, at_place < a.E && tab.pre(at_place) <= rt);
+    const int from = (__popc(m) - 1) * stride;
+    at_place = from + lane;
+    m = __ballot_sync(0xffffffffu, lane < stride && at_place < a.E && tab.pre(at_place) <= rt);
+    const int lo = from + __popc(m) - 1;
     Tile q;
     q.e = tab.order(lo);
     const int c = tab.cnt(q.e), each = tile_rows<CG, BN>(c), at = (rt - tab.pre(lo)) * each;
@@ -449,7 +459,7 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
     if (warp == kMmaWarp) md::tmem_alloc<1>(&sh->tmem, P::kCols);
     read_ranges(tab, a);
     __syncthreads();
-    if (warp == 0) count_tiles<BN>(tab, sh, a);
+    count_tiles<BN>(tab, sh, a);
     md::tmem_fence_before();
     __syncthreads();
     md::tmem_fence_after();
@@ -738,7 +748,7 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
     read_ranges(tab, a);
     __syncthreads();
     sort_experts<MODE>(tab, a);
-    if (!kWg && warp == 0) count_tiles<BN>(tab, sh, a);
+    if (!kWg) count_tiles<BN>(tab, sh, a);
     md::tmem_fence_before();
     md::cluster_sync();
     __syncthreads();
