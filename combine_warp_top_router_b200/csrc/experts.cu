@@ -618,8 +618,8 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
 // GPU take one sub.
 //
 // A stage holds a block of sub 0's A, of x, and of sub 1's A, on one barrier, and
-// A and x have a loading thread each: a thread's instructions around a barrier and
-// its copies took longer than the products when one thread did it all.
+// A and x have a loading warp each: the instructions around a barrier and its copies
+// took longer than the products when one thread did it all.
 //
 // The two accumulators of 256 columns fill TMEM and are used in turn, one for
 // each (tile, sub).  The epilogue's warps take an accumulator into registers and
