@@ -163,12 +163,12 @@ struct Turn {
     }
 };
 
-// Await the copies in flight, whoever gave up: the last load of each stage.
-__device__ __forceinline__ void drain_loads(Turn at, int used, uint64_t *full)
+// Await the copies in flight, whoever gave up: the last load of each stage (or, by `empty`, its last use).
+__device__ __forceinline__ void drain_loads(Turn at, int used, uint64_t *bars)
 {
     for (int j = 0; j < used; ++j) {
         at.back();
-        md::mbar_wait_bounded(&full[at.s], at.parity, kDrainPolls);
+        md::mbar_wait_bounded(&bars[at.s], at.parity, kDrainPolls);
     }
 }
 
@@ -860,6 +860,9 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
                     if (used_tails >> i & 1u) md::mbar_wait_bounded(&b->tail[i], (tails >> i & 1u) ^ 1u, kDrainPolls);
             if (rank == 1 && !ok)
                 for (int j = 0; j < 2000; ++j) __nanosleep(500);
+            // nor may the products' last arrivals, which come from the first CTA, be still on their
+            // way when this CTA's shared memory is given up
+            if (ok && rank == 1) drain_loads(at, used, b->empty);
         } else if (warp == kMmaWarp) {
             // ------------------------------------------------ products
             // Clears the lines from v on, up to the last of `steps` sixteenths, of every box of a stage.
@@ -1069,7 +1072,13 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
     __syncthreads();
     md::cluster_sync();
     md::tmem_fence_after();
-    if (warp == kMmaWarp) md::tmem_free<2>(tmem, 512);
+    if (warp == kMmaWarp) {
+        // The first CTA has seen its last commit arrive at home; the same commit's arrival here
+        // is awaited too, whoever gave up.
+        if (md::cluster_rank() == 1) md::mbar_wait_bounded(&bars.drain, 0, kDrainPolls);
+        __syncwarp();
+        md::tmem_free<2>(tmem, 512);
+    }
 }
 
 // ------------------------------------------------------------------ host

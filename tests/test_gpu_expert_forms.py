@@ -1,0 +1,38 @@
+"""The expert products' kernel forms, one by one and one behind another.
+
+Tolerances are those of the other expert tests: 2^-8 |want| for the rounding to bf16 and
+n 2^-23 S for a float32 sum of n products whose magnitudes add up to S; small integers are
+held bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+import combine_warp_top_router_b200 as md
+
+from _util import DEV
+from test_gpu_experts import groups, ints
+
+pytestmark = pytest.mark.gpu
+
+
+def test_pairs_one_behind_another():
+    """Short calls of the CTA pairs' kernel back to back, each block of one behind a block of
+    another on the same SM, with the few-row form between: nothing that a pair left unfinished
+    may reach the shared memory of the next."""
+    counts = np.random.default_rng(3).integers(65, 140, 80).tolist()
+    off, cnt, rows, spans = groups(counts, seed=3)
+    K, N = 72, 272
+    x, dy = ints(1, rows, K, hi=1), ints(2, rows, N, hi=1)
+    w = ints(3, len(counts), N, K, hi=1)
+    zero, full = torch.zeros(1, dtype=torch.int32, device=DEV), torch.full((1,), 64, dtype=torch.int32, device=DEV)
+    calls = [lambda: md.md_expert_gemm(x, w, off, cnt), lambda: md.md_expert_gemm(dy, w, off, cnt, md.MD_W_KN),
+             lambda: md.md_expert_wgrad(dy, x, off, cnt), lambda: md.md_expert_gated(x, w, off, cnt),
+             lambda: md.md_expert_gemm(x[:64], w[:1], zero, full)]
+    want = [c() for c in calls]
+    for e, o, c in spans:
+        assert torch.equal(want[0][o:o + c].double(), x[o:o + c].double() @ w[e].double().t())
+        assert torch.equal(want[2][e].double(), dy[o:o + c].double().t() @ x[o:o + c].double())
+    order = np.random.default_rng(4).integers(0, len(calls), 1500).tolist()
+    got = [(i, calls[i]()) for i in order]
+    wrong = sum((y.view(torch.uint8) != want[i].view(torch.uint8)).any().long() for i, y in got)
+    assert int(wrong) == 0
