@@ -24,6 +24,7 @@
 // their loops, copies and MMAs in flight are awaited (bounded again), TMEM is
 // freed, and the kernel returns.
 #include "activation.cuh"
+#include "ragged.cuh"
 #include "tcgen05.cuh"
 
 namespace {
@@ -204,9 +205,7 @@ __device__ __forceinline__ void read_ranges(const Table &tab, const Args &a)
 template <int CG, int BN>
 __device__ __forceinline__ int tile_rows(int c)
 {
-    constexpr int kGran = 16 * CG;
-    const int nt = (c + BN - 1) / BN;
-    return nt ? ((c + nt - 1) / nt + kGran - 1) / kGran * kGran : 0;
+    return md::ragged_rows(c, BN, 16 * CG);
 }
 
 // Order the experts by the cost of their tiles, falling (equal: by number), by
@@ -236,7 +235,7 @@ __device__ __forceinline__ void count_tiles(const Table &tab, Shared *sh, const 
     int run = 0;
     for (int e0 = 0; e0 < a.E; e0 += blockDim.x) {
         const int e = e0 + threadIdx.x;
-        const int own = e < a.E ? (tab.cnt(tab.order(e)) + BN - 1) / BN : 0;
+        const int own = e < a.E ? md::ragged_tiles(tab.cnt(tab.order(e)), BN) : 0;
         int v = own;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {

@@ -36,3 +36,28 @@ def test_pairs_one_behind_another():
     got = [(i, calls[i]()) for i in order]
     wrong = sum((y.view(torch.uint8) != want[i].view(torch.uint8)).any().long() for i, y in got)
     assert int(wrong) == 0
+
+
+def test_as_many_rows_as_there_may_be():
+    """One expert with 2^31 - 4097 rows: 69 GB of the smallest rows, zero but at both ends and around
+    the middle."""
+    rows = 2 ** 31 - 4097
+    torch.cuda.empty_cache()
+    x = torch.zeros(rows, 8, dtype=torch.bfloat16, device=DEV)
+    parts = [slice(0, 700), slice(2 ** 30 - 300, 2 ** 30 + 300), slice(rows - 700, rows)]
+    for i, p in enumerate(parts):
+        x[p] = ints(i, p.stop - p.start, 8)
+    w = ints(7, 1, 8, 8)
+    y = torch.full((rows, 8), 9.0, dtype=torch.bfloat16, device=DEV)
+    t = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    st = md.new_status(DEV)
+    md.md_expert_gemm(x, w, t([0, rows]), t([rows]), out=y, dev_status=st)
+    md.check_status(st)
+    for p in parts:
+        assert torch.equal(y[p], (x[p].double() @ w[0].double().t()).to(torch.bfloat16))
+        y[p] = 0
+    whole = y.view(-1).view(torch.int64)
+    for at in range(0, whole.numel(), 1 << 30):
+        assert not bool(whole[at:at + (1 << 30)].any())
+    del x, y, whole
+    torch.cuda.empty_cache()
