@@ -62,6 +62,7 @@ struct Args {
     const int32_t *offsets, *counts;
     int64_t rows;
     int E;
+    int64_t row_tiles;  // gemm, gated: as many as ranges that do not overlap can make
     int n;        // weight rows per expert that tiles cover (gemm: N, gated: F, wgrad: N)
     int k;        // extent of the contraction (gemm, gated: K); wgrad: columns of dw
     int pitch;    // columns of y, or of a
@@ -82,7 +83,7 @@ struct Shared {
     int abort;
     unsigned loads;  // counts up as the loading warp goes on: a sign of life for the other roles' waits
     int tiles;  // ragged row tiles of all experts
-    int sums[12];
+    int64_t sums[12];
 };
 
 // Bounded wait of a converged warp; all lanes get the same answer.  The first look
@@ -227,32 +228,40 @@ __device__ __forceinline__ void sort_experts(const Table &tab, const Args &a)
     __syncthreads();
 }
 
-// Exclusive running sum of the experts' row tiles, by all threads; barriers inside.
+// Exclusive running sum of the experts' row tiles, by all threads; barriers inside.  Ranges that
+// overlap so far that they make more tiles than the rows can (and more than the host
+// has allowed for) are reported, and no tile is left.
 template <int BN>
 __device__ __forceinline__ void count_tiles(const Table &tab, Shared *sh, const Args &a)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    int run = 0;
+    int64_t run = 0;
     for (int e0 = 0; e0 < a.E; e0 += blockDim.x) {
         const int e = e0 + threadIdx.x;
         const int own = e < a.E ? md::ragged_tiles(tab.cnt(tab.order(e)), BN) : 0;
-        int v = own;
+        int64_t v = own;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, v, d);
+            const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
             if (lane >= d) v += o;
         }
         if (lane == 31) sh->sums[warp] = v;
         __syncthreads();
-        int before = run;
+        int64_t before = run;
         for (int w = 0; w < warps; ++w) {
             before += w < warp ? sh->sums[w] : 0;
             run += sh->sums[w];
         }
-        if (e < a.E) tab.pre(e) = before + v - own;
+        if (e < a.E) tab.pre(e) = (int)(before + v - own);
         __syncthreads();
     }
-    if (threadIdx.x == 0) sh->tiles = run;
+    if (threadIdx.x == 0) {
+        if (run > a.row_tiles) {
+            md::report(a.status, MD_ERR_DATA);
+            run = 0;
+        }
+        sh->tiles = (int)run;
+    }
 }
 
 // Rows of row tile rt; a converged warp, which looks at 32 places of the order at once.
@@ -465,8 +474,7 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
     const uint32_t tmem = sh->tmem;
 
     const int first = blockIdx.x / a.split, step = gridDim.x / a.split;
-    int total = sh->tiles * (int)a.mt.d;  // the host keeps it below 2^30
-    if (a.split > 1) total = min(total, step);  // one tile to a cluster, even if ranges overlap
+    const int total = sh->tiles * (int)a.mt.d;  // the host keeps it below 2^30
     const uint32_t sbase = md::smem_addr(base);
     // blocks of the contraction: [kb0, kb1) in this CTA
     const int kblocks = (a.k + kTileK - 1) / kTileK;
@@ -1133,6 +1141,10 @@ bool too_large(int64_t rows, int E, int64_t N, int64_t K)
 
 constexpr int64_t kMostTiles = (int64_t)1 << 30;
 
+// Row tiles of `most` rows that E ranges of `rows` rows make, at most: sum of ceil(c / most)
+// <= rows / most + (experts with rows) (1 - 1 / most).
+int64_t most_row_tiles(int64_t rows, int E, int most) { return rows / most + (rows < E ? rows : E); }
+
 template <int MODE>
 int run_few(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int64_t d1, cudaStream_t s)
 {
@@ -1143,7 +1155,8 @@ int run_few(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int
         return MD_ERR_CUDA;
     const int mt = (a.n + P::kWidth - 1) / P::kWidth;
     a.mt = FastDiv((uint32_t)mt);
-    const int64_t tiles = (rows / P::BN + (rows < a.E ? rows : a.E)) * mt;  // at most
+    a.row_tiles = most_row_tiles(rows, a.E, P::BN);
+    const int64_t tiles = a.row_tiles * mt;
     if (tiles > kMostTiles) return MD_ERR_UNSUPPORTED;
     // Few tiles leave SMs idle and each tile streams its weights through one SM: clusters of
     // CTAs share a tile's contraction, as long as all of them are resident and each has
@@ -1173,13 +1186,13 @@ int run_wide(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, in
     if (!md::make_map(&ma, w, kBf16, 2, d0, d1, a.E, 64, MODE == kNK ? kTileM : 64) ||
         !md::make_map(&mb, x, kBf16, 2, a.k, rows, 0, 64, 64))
         return MD_ERR_CUDA;
-    const int64_t row_tiles = rows / 256 + (rows < a.E ? rows : a.E);  // at most
-    a.subs = subs_for(row_tiles * ((a.n + W::kSub - 1) / W::kSub), 4);
+    a.row_tiles = most_row_tiles(rows, a.E, 256);
+    a.subs = subs_for(a.row_tiles * ((a.n + W::kSub - 1) / W::kSub), 4);
     const int mt = (a.n + a.subs * W::kSub - 1) / (a.subs * W::kSub);
     a.mt = FastDiv((uint32_t)mt);
-    if (row_tiles * mt > kMostTiles) return MD_ERR_UNSUPPORTED;
+    if (a.row_tiles * mt > kMostTiles) return MD_ERR_UNSUPPORTED;
     static std::atomic<uint64_t> setup{0};
-    return launch(k_expert_wide<MODE>, W::kThreads, kLaunchRegisters, W::smem(a.E), W::smem(MD_MAX_EXPERTS), setup, row_tiles * mt, 2, s, ma,
+    return launch(k_expert_wide<MODE>, W::kThreads, kLaunchRegisters, W::smem(a.E), W::smem(MD_MAX_EXPERTS), setup, a.row_tiles * mt, 2, s, ma,
                   mb, mb, a);
 }
 
@@ -1191,7 +1204,7 @@ int run_wide(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, in
 // rows, 1024 x 1024: 11 / 13; of 512 rows 18 / 13).  `sub`: output columns of a wide tile.
 bool few_rows(int64_t rows, int E, int64_t columns, int sub)
 {
-    const int64_t wide = (rows / 256 + (rows < E ? rows : E)) * ((columns + sub - 1) / sub);
+    const int64_t wide = most_row_tiles(rows, E, 256) * ((columns + sub - 1) / sub);
     return rows <= (int64_t)64 * E || wide <= md::sm_count() / 2;
 }
 

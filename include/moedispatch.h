@@ -658,7 +658,10 @@ void md_set_test_hooks(long long poll_limit, int layout_skip_tile, long long exp
  * mode's assign_row order; md_dispatch_permute or md_dedup_expand fills them):
  *   expert_offsets int32 [>= E]  first row of expert e
  *   expert_counts  int32 [E]     rows of expert e; 0 is allowed
- * Experts may stand in any order; their ranges must not overlap.  A range
+ * Experts may stand in any order; their ranges must not overlap (rows of two
+ * experts have no one result; md_expert_gemm and md_expert_gated write nothing
+ * and report MD_ERR_DATA where the ranges make more tiles than `rows` rows
+ * can).  A range
  * that leaves [0, rows) is treated as empty and reported (MD_ERR_DATA).  Rows
  * that belong to no expert are neither read into a result nor written.
  * Products are bf16 x bf16 on the tensor cores with float32 sums, rounded to

@@ -61,3 +61,22 @@ def test_as_many_rows_as_there_may_be():
         assert not bool(whole[at:at + (1 << 30)].any())
     del x, y, whole
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("E,rows,N", [(8, 100, 64), (3, 70, 64), (64, 9000, 1416)])
+@pytest.mark.parametrize("op", ["nk", "kn", "gated"])
+def test_ranges_that_overlap_far_write_nothing(E, rows, N, op):
+    """Every expert claims all rows: more tiles than the rows can make."""
+    K = 512 if E == 3 else 72  # E == 3: a contraction that CTAs share
+    x = ints(1, rows, K)
+    w = ints(2, *((E, K, N) if op == "kn" else (E, 2 * N if op == "gated" else N, K)))
+    cnt = torch.full((E,), rows, dtype=torch.int32, device=DEV)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    st = md.new_status(DEV)
+    y = torch.full((rows, N), 9.0, dtype=torch.bfloat16, device=DEV)
+    if op == "gated":
+        md.md_expert_gated(x, w, off, cnt, out=y, dev_status=st)
+    else:
+        md.md_expert_gemm(x, w, off, cnt, md.MD_W_KN if op == "kn" else md.MD_W_NK, out=y, dev_status=st)
+    assert int(st.item()) == md.MD_ERR_DATA
+    assert bool((y == 9.0).all())
