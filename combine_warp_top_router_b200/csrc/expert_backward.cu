@@ -39,7 +39,7 @@ __device__ __forceinline__ float scale_of(uint32_t s) { return __uint_as_float(s
 // a = g s u.  Float32 throughout, one rounding to bf16 per output.
 // One piece of 8 columns to a thread, and as many threads as pieces: kept threads
 // with a loop ran 14% slower, two pieces at a time as fast.
-// 131072 rows of 1024: 229 us, 5.9 TB/s (60% of it writes).
+// 131072 rows of 1024: 228 us, 5.9 TB/s (60% of it writes).
 __global__ void __launch_bounds__(kThreads)
     k_gated_backward(const uint4 *__restrict__ da, const uint8_t *__restrict__ codes,
                      const uint8_t *__restrict__ scales, int64_t rows, int F, uint4 *__restrict__ dh,

@@ -80,3 +80,39 @@ def test_ranges_that_overlap_far_write_nothing(E, rows, N, op):
         md.md_expert_gemm(x, w, off, cnt, md.MD_W_KN if op == "kn" else md.MD_W_NK, out=y, dev_status=st)
     assert int(st.item()) == md.MD_ERR_DATA
     assert bool((y == 9.0).all())
+
+
+@pytest.mark.parametrize("lo,hi", [(-86, -60), (-60, -46), (-44, -16), (-16, 16), (16, 100)])
+def test_activation_rounds_as_the_exact_one_but_next_to_a_border(lo, hi):
+    """g sigma(g) u in float32 and one rounding to bf16, at a million arguments that float32 sums give
+    exactly.  2^x is good to 4 * 2^-24, its correction to 1 and the float32 ln 2 in it to 4 for g > -87
+    (1.9e-9 a unit of x), which makes 9 where g < -44; above, the last is 2 at most and the sum
+    1 + 2^x (1) and its reciprocal (2) follow, which makes 10.  With two products: 12 * 2^-24.  Where the
+    exact value is further from the border between two bf16 values, the result must be the nearer one."""
+    rows, F, K = 32, 8192, 64
+    g = torch.Generator(device=DEV).manual_seed(100 + lo)
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device=DEV)
+    x[torch.arange(rows), 2 * torch.arange(rows)] = 1
+    x[torch.arange(rows), 2 * torch.arange(rows) + 1] = 1
+    t = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    wrong = near = 0
+    for _ in range(4):
+        # two summands each, 16 bits together: every order of summing is exact
+        low = torch.randint(-127, 128, (2 * F, K), generator=g, device=DEV).double()
+        w = torch.empty(2 * F, K, dtype=torch.float64, device=DEV)
+        w[:F] = (lo + (hi - lo) * torch.rand(F, K, generator=g, device=DEV)).to(torch.bfloat16).double()
+        w[F:] = ((1 + torch.rand(F, K, generator=g, device=DEV)) * 2.0 ** 20).to(torch.bfloat16).double()
+        w[:F, 1::2] = low[:F, 1::2] * 2.0 ** -9
+        w[F:, 1::2] = low[F:, 1::2] * 2.0 ** 5
+        if lo == -16:  # 8 bits around 0 reach further down than 2^-9
+            w[:F, 0::2] = (w[:F, 0::2] * 16).round() / 16
+        act = md.md_expert_gated(x, w.to(torch.bfloat16)[None].contiguous(), t([0, rows]), t([rows]))
+        h = (w[:, 0::2] + w[:, 1::2]).t()
+        want = h[:, :F] / (1 + torch.exp(-h[:, :F])) * h[:, F:]
+        tol = 12 * 2.0 ** -24 * want.abs()
+        low_end, high_end = (want - tol).to(torch.bfloat16), (want + tol).to(torch.bfloat16)
+        sure = low_end == high_end
+        near += int((~sure).sum())
+        wrong += int((sure & (act != low_end)).sum())
+    assert near < 4 * rows * F * 0.01  # the borders' share: 2 * 12 * 2^-24 of 2^-8
+    assert wrong == 0, wrong
