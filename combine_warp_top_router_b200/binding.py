@@ -29,6 +29,7 @@ MD_PERMUTE_AUTO, MD_PERMUTE_BULK, MD_PERMUTE_VECTOR = 0, 1, 2
 MD_LAYOUT_AUTO, MD_LAYOUT_COOPERATIVE, MD_LAYOUT_SPLIT = 0, 1, 2
 MD_W_NK, MD_W_KN = 0, 1
 MD_F32, MD_BF16 = 0, 1
+MD_EXPERT_AUTO, MD_EXPERT_FEW, MD_EXPERT_ONE, MD_EXPERT_TWO = 0, 1, 2, 3
 MD_CHECKPOINT_BLOCK = 32  # columns that share a scale of the 8-bit checkpoint
 
 _lock = threading.Lock()
@@ -78,6 +79,7 @@ _SIGNATURES = {
     "md_expert_gemm": ([_P, _L, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P], _I),
     "md_expert_gated": ([_P, _L, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
     "md_expert_wgrad": ([_P, _P, _L, _I, _I, _I, _P, _P, _I, _I, _P, _P, _P], _I),
+    "md_set_expert_path": ([_I], _I),
     "md_expert_gated_backward": ([_P, _P, _P, _L, _I, _P, _P, _P], _I),
     "md_combine_backward": ([_P, _P, _L, _P, _P, _L, _I, _I, _P, _P, _P, _P], _I),
     "md_gather_rows": ([_P, _L, _L, _P, _L, _P, _P, _P], _I),
@@ -636,6 +638,11 @@ def _tail(dev_status, stream, dev):
 
 # the current stream's handle without the Stream object around it (2 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def md_set_expert_path(path=MD_EXPERT_AUTO):
+    """Choose the kernel form of the expert products (tests and tuning)."""
+    _check(_call("md_set_expert_path", "cpu", int(path)), "md_set_expert_path")
 
 
 def md_expert_gemm(x, w, expert_offsets, expert_counts, w_layout=MD_W_NK, out=None,

@@ -26,6 +26,8 @@ static std::atomic<int> g_permute_path{MD_PERMUTE_AUTO};
 int permute_path() { return g_permute_path.load(std::memory_order_relaxed); }
 static std::atomic<int> g_layout_path{MD_LAYOUT_AUTO};
 int layout_path() { return g_layout_path.load(std::memory_order_relaxed); }
+static std::atomic<int> g_expert_path{MD_EXPERT_AUTO};
+int expert_path() { return g_expert_path.load(std::memory_order_relaxed); }
 }  // namespace md
 
 extern "C" int md_set_layout_path(int path)
@@ -41,6 +43,13 @@ extern "C" int md_set_permute_path(int path)
     if (path != MD_PERMUTE_AUTO && path != MD_PERMUTE_BULK && path != MD_PERMUTE_VECTOR)
         return MD_ERR_ARG;
     md::g_permute_path.store(path, std::memory_order_relaxed);
+    return MD_OK;
+}
+
+extern "C" int md_set_expert_path(int path)
+{
+    if (path < MD_EXPERT_AUTO || path > MD_EXPERT_TWO) return MD_ERR_ARG;
+    md::g_expert_path.store(path, std::memory_order_relaxed);
     return MD_OK;
 }
 

@@ -1175,6 +1175,8 @@ int run_few(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int
 // from eight (8 experts of 256 rows, 2048 x 2048: 32 / 37; 16 of 512 rows 86 / 79).
 inline int subs_for(int64_t tiles_of_one, int to_a_pair)
 {
+    const int path = md::expert_path();
+    if (path == MD_EXPERT_ONE || path == MD_EXPERT_TWO) return path == MD_EXPERT_TWO ? 2 : 1;
     return tiles_of_one >= (int64_t)to_a_pair * (md::sm_count() / 2) ? 2 : 1;
 }
 
@@ -1204,6 +1206,8 @@ int run_wide(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, in
 // rows, 1024 x 1024: 11 / 13; of 512 rows 18 / 13).  `sub`: output columns of a wide tile.
 bool few_rows(int64_t rows, int E, int64_t columns, int sub)
 {
+    const int path = md::expert_path();
+    if (path != MD_EXPERT_AUTO) return path == MD_EXPERT_FEW;
     const int64_t wide = most_row_tiles(rows, E, 256) * ((columns + sub - 1) / sub);
     return rows <= (int64_t)64 * E || wide <= md::sm_count() / 2;
 }

@@ -722,6 +722,24 @@ int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int E, int N, i
                     int accumulate, void *dw, int32_t *dev_status, void *stream);
 
 /*
+ * md_set_expert_path -- which kernel form the three products run (for tests and
+ * tuning; results differ by the order of float32 sums at most).
+ *   MD_EXPERT_AUTO  by shape (default)
+ *   MD_EXPERT_FEW   tiles of 128 weight rows by up to 64 rows, one CTA each
+ *                   (md_expert_wgrad has no such form and goes by shape)
+ *   MD_EXPERT_ONE   CTA pairs, tiles of 256 weight rows by up to 256 rows
+ *   MD_EXPERT_TWO   CTA pairs, two such tiles at once that share their rows
+ * Process-wide; MD_ERR_ARG for another value.  Set it only while no such call
+ * is being enqueued.
+ */
+#define MD_EXPERT_AUTO 0
+#define MD_EXPERT_FEW 1
+#define MD_EXPERT_ONE 2
+#define MD_EXPERT_TWO 3
+
+int md_set_expert_path(int path);
+
+/*
  * md_expert_gated_backward -- the activation's gradient from the checkpoint of
  * md_expert_gated.  With g, u the checkpoint's values and s = 1/(1+exp(-g)):
  *   dh[r][f]     = bf16( da[r][f] u s (1 + g (1 - s)) )    (gradient of g)

@@ -1,6 +1,8 @@
 """The expert products' kernel forms, one by one and one behind another.
 
-Tolerances are those of the other expert tests: 2^-8 |want| for the rounding to bf16 and
+Which form a call takes goes by its shape, and the smaller shapes of the other expert tests all take the
+few-row form; here those tests run again in the two forms for many rows, and in cases that
+only these meet.  Tolerances are those of the other tests: 2^-8 |want| for the rounding to bf16 and
 n 2^-23 S for a float32 sum of n products whose magnitudes add up to S; small integers are
 held bit for bit."""
 import numpy as np
@@ -8,12 +10,151 @@ import pytest
 import torch
 
 import combine_warp_top_router_b200 as md
+import test_gpu_experts as base
 
 from _util import DEV
-from test_gpu_experts import groups, ints
+from test_gpu_experts import close, groups, ints, owned, products64, randn
 
 pytestmark = pytest.mark.gpu
 
+
+@pytest.fixture(params=[md.MD_EXPERT_ONE, md.MD_EXPERT_TWO], ids=["one", "two"])
+def pairs(request):
+    """CTA pairs with one product to a tile, and with two."""
+    md.md_set_expert_path(request.param)
+    yield request.param
+    md.md_set_expert_path(md.MD_EXPERT_AUTO)
+
+
+@pytest.fixture(params=[md.MD_EXPERT_FEW, md.MD_EXPERT_ONE, md.MD_EXPERT_TWO], ids=["few", "one", "two"])
+def form(request):
+    md.md_set_expert_path(request.param)
+    yield request.param
+    md.md_set_expert_path(md.MD_EXPERT_AUTO)
+
+
+def test_another_form_is_refused():
+    for bad in (-1, 4):
+        with pytest.raises(md.MoeDispatchError) as err:
+            md.md_set_expert_path(bad)
+        assert err.value.code == md.MD_ERR_ARG
+    md.md_set_expert_path(md.MD_EXPERT_AUTO)
+
+
+# ------------------------------------------------------------------ the other tests' cases
+
+@pytest.mark.parametrize("layout", [md.MD_W_NK, md.MD_W_KN])
+@pytest.mark.parametrize("counts,K,N", base.SHAPES)
+def test_gemm(pairs, counts, K, N, layout):
+    base.test_gemm(counts, K, N, layout)
+
+
+@pytest.mark.parametrize("layout", [md.MD_W_NK, md.MD_W_KN])
+@pytest.mark.parametrize("counts,K,N", [([7, 0, 33], 128, 136), ([260, 31, 0, 512], 320, 264), ([257, 300], 1032, 1048)])
+def test_exact_on_small_integers_and_other_rows_left(pairs, counts, K, N, layout):
+    base.test_gemm_is_exact_on_small_integers_and_leaves_other_rows(counts, K, N, layout)
+
+
+@pytest.mark.parametrize("op", ["nk", "kn", "gated"])
+@pytest.mark.parametrize("counts,K,N", [([500] + [0] * 62 + [3], 200, 136), ([1, 0, 2], 2056, 264), ([0, 64, 1, 0], 1000, 136),
+                                        ([1] * 200 + [0] * 823 + [7], 72, 64), ([300] * 80, 64, 1032),
+                                        ([257] * 9 + [0, 513], 456, 776)])
+def test_exact_on_small_integers(form, counts, K, N, op):
+    base.test_forms_are_exact_on_small_integers(counts, K, N, op)
+
+
+def test_nan_and_inf_stay_in_their_row_and_expert(pairs):
+    base.test_gemm_keeps_nan_and_inf_to_their_row_and_expert()
+
+
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("counts,K,F", base.GATED + [([300, 0, 700, 5], 648, 520)])
+def test_gated(pairs, counts, K, F, keep):
+    base.test_gated(counts, K, F, keep)
+
+
+@pytest.mark.parametrize("counts,F", [([5, 0, 2], 40), ([300, 20], 96), ([33, 290], 392)])
+def test_checkpoint_is_exact_where_the_sums_are(form, counts, F):
+    base.test_checkpoint_is_exact_where_the_sums_are(counts, F)
+
+
+def test_checkpoint_stores_inf_and_nan_as_nan(pairs):
+    base.test_checkpoint_stores_inf_and_nan_as_nan()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("counts,N,K", [
+    ([1], 8, 8), ([0, 3, 0, 1], 136, 72), ([16, 17, 15, 0, 64, 65], 264, 264), ([300, 0, 257, 256, 1, 255], 392, 520),
+    ([2, 1, 700], 1416, 200), ([63, 64, 65, 127, 129], 776, 1032)])
+def test_wgrad(pairs, counts, N, K, dtype):
+    base.test_wgrad(counts, N, K, dtype)
+
+
+def test_bad_ranges_are_empty_and_reported(pairs):
+    base.test_bad_ranges_are_empty_and_reported()
+
+
+def test_rows_but_no_expert_has_any(pairs):
+    base.test_rows_but_no_expert_has_any()
+
+
+@pytest.mark.parametrize("op", ["nk", "kn", "gated", "wgrad"])
+def test_many_tiles(pairs, op):
+    base.test_many_tiles_of_two_products(op)
+
+
+@pytest.mark.parametrize("hi", [1, 63, 130])
+def test_wgrad_of_many_short_experts(pairs, hi):
+    base.test_wgrad_of_many_short_experts(hi)
+
+
+def test_a_layer_forward_and_backward(form):
+    base.test_a_layer_forward_and_backward_against_autograd_in_64_bits()
+
+
+def test_a_wait_that_runs_out(pairs):
+    base.test_a_wait_that_runs_out_is_reported_and_leaves_the_gpu_usable()
+
+
+# ------------------------------------------------------------------ long contractions and experts
+
+@pytest.mark.parametrize("op", ["nk", "kn"])
+def test_long_contractions_of_ragged_experts(form, op):
+    """Rings that wrap many times, tiles of every remainder, the last weight tile part empty."""
+    counts, K, N = [129, 0, 256, 31, 257, 1, 64, 770, 33], 2056, 1160
+    off, cnt, rows, spans = groups(counts, seed=4, gap=2)
+    nk = op == "nk"
+    x, w = randn(1, rows, K), randn(2, *((len(counts), N, K) if nk else (len(counts), K, N)))
+    st = md.new_status(DEV)
+    y = md.md_expert_gemm(x, w, off, cnt, md.MD_W_NK if nk else md.MD_W_KN, dev_status=st)
+    md.check_status(st)
+    want, mags = products64(x, w, spans, nk)
+    close(y, want, mags, K, owned(rows, spans))
+
+
+@pytest.mark.parametrize("counts,N,K", [([5000, 0, 1153, 1152, 100, 2305], 264, 520), ([2400] * 6 + [1, 0, 64], 776, 264),
+                                        ([3000, 63, 4100], 520, 24)])
+def test_wgrad_of_long_experts(pairs, counts, N, K):
+    """Several parts to an expert, between experts of one part or none: fresh, added twice, in bf16, and
+    with rows of nobody between that are not numbers."""
+    off, cnt, rows, spans = groups(counts, seed=5, gap=3)
+    dy, x = ints(1, rows, N, hi=2), ints(2, rows, K, hi=2)
+    mine = owned(rows, spans)
+    dy[~mine], x[~mine] = float("inf"), float("nan")
+    want = torch.zeros(len(counts), N, K, dtype=torch.float64, device=DEV)
+    for e, o, c in spans:
+        want[e] = dy[o:o + c].double().t() @ x[o:o + c].double()
+    st = md.new_status(DEV)
+    dw = md.md_expert_wgrad(dy, x, off, cnt, dev_status=st)
+    md.check_status(st)
+    assert torch.equal(dw.double(), want)
+    for more in (2, 3):
+        md.md_expert_wgrad(dy, x, off, cnt, dw=dw, accumulate=True)
+        assert torch.equal(dw.double(), more * want)
+    assert torch.equal(md.md_expert_wgrad(dy, x, off, cnt, out_dtype=torch.bfloat16), want.to(torch.bfloat16))
+
+
+# ------------------------------------------------------------------ one behind another, extremes
 
 def test_pairs_one_behind_another():
     """Short calls of the CTA pairs' kernel back to back, each block of one behind a block of
