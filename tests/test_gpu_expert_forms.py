@@ -154,6 +154,25 @@ def test_wgrad_of_long_experts(pairs, counts, N, K):
     assert torch.equal(md.md_expert_wgrad(dy, x, off, cnt, out_dtype=torch.bfloat16), want.to(torch.bfloat16))
 
 
+def test_wgrad_of_a_long_expert_is_as_exact_as_of_a_short_one(pairs):
+    """Normal data, errors in the 2-norm.  An expert of 1152 rows is one part: 72 products of 16 rows, each
+    addition off by 2^-23 of the larger of the running sum, 4 sqrt(i) times a product's deviation, and
+    of a product, taken as 4 times it: sum(4 sqrt(i) + 4) = 1930 against the result's sqrt(1152) = 34 is
+    57 * 2^-23.  Of 40 parts the errors are independent, so that relative to the sum they are as one part's,
+    and 39 float32 additions round to nearest, independently too: sqrt(40) * 2^-24 holds them.  10% for
+    chance (137,000 outputs).  Summed whole, the error grows with the number of products: 40 times."""
+    N, K, one = 264, 520, 1152
+    errs = []
+    for parts in (1, 40):
+        rows = parts * one
+        off, cnt, rows, _ = groups([rows])
+        dy, x = randn(parts, rows, N), randn(parts + 1, rows, K)
+        want = dy.double().t() @ x.double()
+        errs.append(float((md.md_expert_wgrad(dy, x, off, cnt)[0].double() - want).norm() / want.norm()))
+    assert errs[0] < 57 * 2.0 ** -23, errs
+    assert errs[1] < 1.1 * (errs[0] ** 2 + 40 * 2.0 ** -48) ** 0.5, errs
+
+
 # ------------------------------------------------------------------ one behind another, extremes
 
 def test_pairs_one_behind_another():
