@@ -33,6 +33,13 @@ inline cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// whether two buffers of so many bytes share one (NULL shares none)
+inline bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes)
+{
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return a && b && a_bytes > 0 && b_bytes > 0 && p < q + (uint64_t)b_bytes && q < p + (uint64_t)a_bytes;
+}
+
 // Report a failed launch; clears the error so later calls are not blamed.
 inline int launch_status()
 {

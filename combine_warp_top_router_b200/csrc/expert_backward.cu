@@ -165,6 +165,12 @@ extern "C" int md_expert_gated_backward(const void *da, const void *codes, const
     if (!da || !codes || !scales || !dh || !md::aligned16(da) || !md::aligned16(codes) || !md::aligned16(dh) ||
         !md::aligned16(act))
         return MD_ERR_ARG;
+    const int64_t n = rows * F * 2;  // bytes of da, of the codes, of act, and half of dh's
+    const int64_t m = rows * 2 * ((F + kBlock - 1) / kBlock);
+    if (md::overlap(dh, 2 * n, da, n) || md::overlap(dh, 2 * n, codes, n) || md::overlap(dh, 2 * n, scales, m) ||
+        md::overlap(act, n, da, n) || md::overlap(act, n, codes, n) || md::overlap(act, n, scales, m) ||
+        md::overlap(dh, 2 * n, act, n))
+        return MD_ERR_ARG;
     cudaStream_t s = md::as_stream(stream);
     k_gated_backward<<<grid_for(rows * (F / 8), kThreads), kThreads, 0, s>>>(
         static_cast<const uint4 *>(da), static_cast<const uint8_t *>(codes), scales, rows, F,
@@ -181,6 +187,9 @@ extern "C" int md_combine_backward(const void *dout, const void *y, int64_t y_ro
     if (T > 0 && (!dout || !md::aligned16(dout) || !assign_row || !topk_w)) return MD_ERR_ARG;
     if (y_rows > 0 && (!dy || !md::aligned16(dy))) return MD_ERR_ARG;
     if (dw && y_rows > 0 && (!y || !md::aligned16(y))) return MD_ERR_ARG;
+    const int64_t row = (int64_t)H * 2;
+    if (T > 0 && (md::overlap(dy, y_rows * row, dout, T * row) || (dw && md::overlap(dy, y_rows * row, y, y_rows * row))))
+        return MD_ERR_ARG;
     cudaStream_t s = md::as_stream(stream);
     const int rc = md::clear_status(dev_status, s);
     if (rc != MD_OK || T == 0) return rc;

@@ -1222,6 +1222,7 @@ extern "C" int md_expert_gemm(const void *x, int64_t rows, int K, const void *w,
     if (!w || !md::aligned16(w) || !expert_offsets || !expert_counts) return MD_ERR_ARG;
     if (rows > 0 && (!x || !y || !md::aligned16(x) || !md::aligned16(y))) return MD_ERR_ARG;
     if (too_large(rows, E, N, K)) return MD_ERR_UNSUPPORTED;
+    if (md::overlap(y, rows * N * 2, x, rows * K * 2) || md::overlap(y, rows * N * 2, w, (int64_t)E * N * K * 2)) return MD_ERR_ARG;
     cudaStream_t s = md::as_stream(stream);
     const int rc = md::clear_status(dev_status, s);
     if (rc != MD_OK || rows == 0) return rc;
@@ -1253,6 +1254,14 @@ extern "C" int md_expert_gated(const void *x, int64_t rows, int K, const void *w
     if (rows > 0 && (!x || !act || !md::aligned16(x) || !md::aligned16(act))) return MD_ERR_ARG;
     if (codes && !md::aligned16(codes)) return MD_ERR_ARG;
     if (too_large(rows, E, 2 * (int64_t)F, K)) return MD_ERR_UNSUPPORTED;
+    const int64_t wide = rows * F * 2, kept = rows * 2 * ((F + kBlock - 1) / kBlock);  // act and codes; scales
+    const struct { const void *at; int64_t bytes; } in[2] = {{x, rows * K * 2}, {w, (int64_t)E * F * K * 4}};
+    for (const auto &i : in)
+        if (md::overlap(act, wide, i.at, i.bytes) || md::overlap(codes, wide, i.at, i.bytes) ||
+            md::overlap(scales, kept, i.at, i.bytes))
+            return MD_ERR_ARG;
+    if (md::overlap(act, wide, codes, wide) || md::overlap(act, wide, scales, kept) || md::overlap(codes, wide, scales, kept))
+        return MD_ERR_ARG;
     cudaStream_t s = md::as_stream(stream);
     const int rc = md::clear_status(dev_status, s);
     if (rc != MD_OK || rows == 0) return rc;
@@ -1283,14 +1292,16 @@ extern "C" int md_expert_wgrad(const void *dy, const void *x, int64_t rows, int 
     if (!dw || !md::aligned16(dw) || !expert_offsets || !expert_counts) return MD_ERR_ARG;
     if (rows > 0 && (!dy || !x || !md::aligned16(dy) || !md::aligned16(x))) return MD_ERR_ARG;
     if (too_large(rows, E, N, K)) return MD_ERR_UNSUPPORTED;
+    const int size = out_type == MD_F32 ? 4 : 2;
+    const int64_t bytes = (int64_t)E * N * K * size;
+    if (md::overlap(dw, bytes, dy, rows * N * 2) || md::overlap(dw, bytes, x, rows * K * 2)) return MD_ERR_ARG;
     cudaStream_t s = md::as_stream(stream);
     const int rc = md::clear_status(dev_status, s);
     if (rc != MD_OK) return rc;
-    const int size = out_type == MD_F32 ? 4 : 2;
     if (rows == 0) {
         if (accumulate) return MD_OK;
         md::count_memsets(1);
-        return cudaMemsetAsync(dw, 0, (size_t)E * N * K * size, s) == cudaSuccess ? MD_OK : MD_ERR_CUDA;
+        return cudaMemsetAsync(dw, 0, (size_t)bytes, s) == cudaSuccess ? MD_OK : MD_ERR_CUDA;
     }
     Args a = {};
     a.split = 1;

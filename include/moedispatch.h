@@ -667,6 +667,7 @@ void md_set_test_hooks(long long poll_limit, int layout_skip_tile, long long exp
  * Products are bf16 x bf16 on the tensor cores with float32 sums, rounded to
  * the output type once.  NaN or Inf in one row reaches that row's results
  * only (md_expert_wgrad: its expert's).
+ * Outputs must overlap neither inputs nor each other (MD_ERR_ARG).
  * Limits of the three products: N, K (gated: F, K) multiples of 8, N (gated:
  * 2F) and K up to 2^20, N * K <= 2^37; E <= 1024; rows < 2^31 - 4096; all buffers 16-byte
  * aligned.  The waits inside the kernels are bounded (MD_ERR_TIMEOUT).  One
@@ -749,7 +750,7 @@ int md_set_expert_path(int path);
  *   da bf16 [rows, F], codes e4m3 [rows, 2F], scales uint8 [rows, 2*ceil(F/32)],
  *   dh bf16 [rows, 2F], act bf16 [rows, F]; float32 inside.
  * A NaN code gives NaN.  F a multiple of 8; da, codes, dh, act 16-byte
- * aligned.
+ * aligned.  Outputs must overlap neither inputs nor each other (MD_ERR_ARG).
  */
 int md_expert_gated_backward(const void *da, const void *codes, const uint8_t *scales, int64_t rows,
                              int F, void *dh, void *act, void *stream);
@@ -766,8 +767,8 @@ int md_expert_gated_backward(const void *da, const void *codes, const uint8_t *s
  *   dw          float32 [T, k]       out, or NULL: sum_h dout[t][h] y[row][h],
  *                                    summed in float32 in a fixed order
  * A row index outside [0, y_rows) is skipped and reported (MD_ERR_DATA), its
- * dw is 0.  No row is named twice (as in a layout); dy must not overlap y or
- * dout.
+ * dw is 0.  No row is named twice (as in a layout); dy must overlap neither y
+ * nor dout (MD_ERR_ARG).
  */
 int md_combine_backward(const void *dout, const void *y, int64_t y_rows, const int32_t *assign_row,
                         const float *topk_w, int64_t T, int k, int H, void *dy, float *dw,

@@ -70,3 +70,19 @@ def test_calls_without_rows_enqueue_nothing():
     assert backward(rows=0, da=None, codes=None, scales=None, dh=None) == OK
     assert combine(T=0, dout=None, rows=None, w=None) == OK
     assert L().md_launch_count() == before
+
+
+@pytest.mark.parametrize("call,args", [
+    (gemm, dict(y=P)), (gemm, dict(x=P, w=16 * P, y=P + 10 * 64 * 2 - 16)), (gemm, dict(x=16 * P, w=P, y=P + 4 * 64 * 64 * 2 - 16)),
+    (gemm, dict(x=P + 16, w=16 * P, y=P)),
+    (gated, dict(x=P, w=16 * P, act=P, codes=None, scales=None)), (gated, dict(x=P, w=16 * P, act=32 * P, codes=P + 1264, scales=64 * P)),
+    (gated, dict(x=P, w=16 * P, act=32 * P, codes=48 * P, scales=16 * P + 4 * 128 * 64 * 2 - 1)),
+    (gated, dict(x=P, w=16 * P, act=32 * P, codes=32 * P + 1264, scales=64 * P)),
+    (gated, dict(x=P, w=16 * P, act=32 * P, codes=48 * P, scales=48 * P + 10 * 128 - 1)),
+    (wgrad, dict(dy=P, x=16 * P, dw=P)), (wgrad, dict(dy=P, x=16 * P, dw=16 * P - 4 * 64 * 64 * 4 + 16)),
+    (backward, dict(da=P, codes=2 * P, scales=3 * P, dh=4 * P, act=P)), (backward, dict(da=P, codes=2 * P, scales=3 * P, dh=P + 1264, act=None)),
+    (backward, dict(da=P, codes=2 * P, scales=3 * P, dh=4 * P, act=4 * P + 2 * 1280 - 16)),
+    (backward, dict(da=P, codes=2 * P, scales=4 * P + 2 * 1280 - 1, dh=4 * P, act=None)),
+    (combine, dict(dout=2 * P, y=P, dy=P)), (combine, dict(dout=P, y=None, dw=None, dy=P + 5 * 64 * 2 - 16))])
+def test_outputs_on_top_of_inputs_or_each_other(call, args):
+    assert call(**args) == ARG
