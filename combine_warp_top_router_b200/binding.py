@@ -772,7 +772,7 @@ def md_combine_backward(dout, assign_row, topk_w, y=None, y_rows=None, dy=None, 
     """Gradient of md_combine: (dy, dw), dy[assign_row[t, j]] = topk_w[t, j] dout[t].
 
     dw [T, k] is the gates' gradient; it needs the expert outputs y (without y it is None).
-    dy has y's rows, or y_rows (default T * k)."""
+    dy has y_rows rows: y's, or without y dy's or T * k by default."""
     dev = _first(dout, "dout", torch.bfloat16, 2)
     T, H = dout.shape
     _need(topk_w, "topk_w", torch.float32, dev)
@@ -781,7 +781,8 @@ def md_combine_backward(dout, assign_row, topk_w, y=None, y_rows=None, dy=None, 
     k = topk_w.shape[1]
     _exact(assign_row, "assign_row", torch.int32, dev, (T, k))
     if y is not None:
-        y_rows = y.shape[0]
+        if y_rows is None and isinstance(y, torch.Tensor) and y.dim() == 2:
+            y_rows = y.shape[0]
         _exact(y, "y", torch.bfloat16, dev, (y_rows, H))
         if dw is None:
             dw = torch.empty_like(topk_w)

@@ -859,3 +859,22 @@ def test_first_call_may_be_captured(op):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, call())
+
+
+def test_combine_backward_refuses_rows_that_are_not_ys():
+    T, k, H = 4, 2, 64
+    dout, y = randn(1, T, H), randn(2, T * k, H)
+    rows = torch.arange(T * k, dtype=torch.int32, device=DEV).view(T, k)
+    w = torch.rand(T, k, device=DEV)
+    for bad in (T * k + 3, T * k - 1):
+        with pytest.raises(ValueError):
+            md.md_combine_backward(dout, rows, w, y, y_rows=bad)
+        with pytest.raises(ValueError):
+            md.md_combine_backward(dout, rows, w, y_rows=bad, dy=torch.empty_like(y))
+    with pytest.raises(TypeError):
+        md.md_combine_backward(dout, rows, w, y.tolist())
+    with pytest.raises(ValueError):
+        md.md_combine_backward(dout, rows, w, y[0].contiguous())
+    dy, dw = md.md_combine_backward(dout, rows, w, y, y_rows=T * k)
+    again = md.md_combine_backward(dout, rows, w, y)
+    assert torch.equal(dy, again[0]) and torch.equal(dw, again[1])
