@@ -2,13 +2,14 @@
 
 Argument marshalling only: every function checks tensor placement, dtype and
 contiguity, allocates outputs with torch when the caller passes none, and calls
-the C entry point of the same name on the current CUDA stream.  All arithmetic
-runs in the library's kernels.  If libmoedispatch.so is missing the first call
+the C entry point of the same name on the current CUDA stream, or as in
+`torch.cuda.stream(stream)` where `stream=` is given.  All arithmetic runs in the library's kernels.  If libmoedispatch.so is missing the first call
 raises; there is no fallback.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -157,6 +158,23 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+# the current stream's handle without the Stream object around it (2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on_its_stream(fn):
+    """With `stream=` given the call runs as in `torch.cuda.stream(stream)`: what it allocates, outputs
+    and scratch, then belongs to that stream.  Memory of the current stream may be freed there while
+    kernels still use it, and the call on the other stream would write into it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None or (_raw_stream is not None and _raw_stream(stream.device_index) == stream.cuda_stream):
+            return fn(*args, stream=stream, **kw)  # already the current one
+        with torch.cuda.stream(stream):
+            return fn(*args, stream=stream, **kw)
+    return call
+
+
 def _need(t, name, dtype, device=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -192,6 +210,7 @@ def check_status(dev_status: torch.Tensor, what: str = "device status"):
 
 # ------------------------------------------------------------------ router
 
+@_on_its_stream
 def md_route_topk(logits, k, gate_mode=MD_GATE_TOPK_SOFTMAX, topk_idx=None, topk_w=None,
                   stream=None):
     _need(logits, "logits", torch.float32)
@@ -259,6 +278,7 @@ def alloc_workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+@_on_its_stream
 def md_dispatch_layout(topk_idx, E, R, expert_to_rank, mode, out: Layout | None = None,
                        workspace=None, dev_status=None, stream=None) -> Layout:
     _need(topk_idx, "topk_idx", torch.int32)
@@ -282,6 +302,7 @@ def md_dispatch_layout(topk_idx, E, R, expert_to_rank, mode, out: Layout | None 
     return out
 
 
+@_on_its_stream
 def md_dispatch_layout_noalloc(topk_idx, E, R, expert_to_rank, mode, out: Layout | None = None,
                                dev_status=None, stream=None) -> Layout:
     """md_dispatch_layout without a workspace, for callers that cannot allocate
@@ -305,6 +326,7 @@ def md_dispatch_layout_noalloc(topk_idx, E, R, expert_to_rank, mode, out: Layout
 
 # --------------------------------------------------------- permute/combine
 
+@_on_its_stream
 def md_dispatch_permute(x, row_of_slot, out_rows=None, out=None, dev_status=None, stream=None):
     _need(x, "x", torch.bfloat16)
     dev = x.device
@@ -333,6 +355,7 @@ def md_set_layout_path(path=MD_LAYOUT_AUTO):
     _check(lib().md_set_layout_path(int(path)), "md_set_layout_path")
 
 
+@_on_its_stream
 def md_dedup_expand(wire, row_of_slot, assign_row, out_rows=None, out=None, dev_status=None,
                     stream=None):
     """out[assign_row[t, j]] = wire[row_of_slot[t, j]]: dedup rows to expert-grouped rows."""
@@ -356,6 +379,7 @@ def md_dedup_expand(wire, row_of_slot, assign_row, out_rows=None, out=None, dev_
     return out
 
 
+@_on_its_stream
 def md_combine(y, assign_row, topk_idx, topk_w, mode=MD_COMBINE_FUSED, row_of_slot=None, z=None,
                out=None, dev_status=None, stream=None):
     _need(y, "y", torch.bfloat16)
@@ -384,6 +408,7 @@ def md_combine(y, assign_row, topk_idx, topk_w, mode=MD_COMBINE_FUSED, row_of_sl
     return out
 
 
+@_on_its_stream
 def md_gather_rows(src, index, out=None, dev_status=None, stream=None):
     if not src.is_cuda or not src.is_contiguous():
         raise ValueError("src must be a contiguous CUDA tensor")
@@ -405,6 +430,7 @@ def md_gather_rows(src, index, out=None, dev_status=None, stream=None):
 
 # --------------------------------------------------- statistics / planning
 
+@_on_its_stream
 def md_coselect_stats(idx_l, idx_next, E, T_fit=None, W=None, C=None, accumulate=False,
                       want_W=True, want_C=True, dev_status=None, stream=None):
     _need(idx_l, "idx_l", torch.int32)
@@ -435,6 +461,7 @@ def md_coselect_stats(idx_l, idx_next, E, T_fit=None, W=None, C=None, accumulate
     return W, C
 
 
+@_on_its_stream
 def md_place_correlated(W, R, seed_mode=MD_SEED_CONTIGUOUS, refine=True, out=None,
                         workspace=None, dev_status=None, stream=None):
     _need(W, "W", torch.int32)
@@ -456,6 +483,7 @@ def md_place_correlated(W, R, seed_mode=MD_SEED_CONTIGUOUS, refine=True, out=Non
     return out
 
 
+@_on_its_stream
 def md_place_two_level(W, R, nodes=1, seed_mode=MD_SEED_CONTIGUOUS, refine_mode=MD_REFINE_SWAPS,
                        out=None, workspace=None, dev_status=None, stream=None):
     """Placement over `nodes` nodes of R/nodes ranks (nodes=1: one level), with no
@@ -488,6 +516,7 @@ def _shuffle_checks(C, E, p_next, T, dev, **outs):
         _room(t, name, T)
 
 
+@_on_its_stream
 def md_token_shuffle(idx_l, C, expert_to_rank_next, R, pred_rank=None, perm=None, inv=None,
                      workspace=None, dev_status=None, stream=None):
     _need(idx_l, "idx_l", torch.int32)
@@ -511,6 +540,7 @@ def md_token_shuffle(idx_l, C, expert_to_rank_next, R, pred_rank=None, perm=None
     return pred_rank, perm, inv
 
 
+@_on_its_stream
 def md_token_shuffle_rounds(idx_l, C, expert_to_rank_next, R, pred_rank=None, perm=None,
                             inv=None, workspace=None, dev_status=None, stream=None):
     """Rounds-based capacity assignment -> (pred, perm, inv, rounds [1] device tensor)."""
@@ -537,6 +567,7 @@ def md_token_shuffle_rounds(idx_l, C, expert_to_rank_next, R, pred_rank=None, pe
     return pred_rank, perm, inv, rounds
 
 
+@_on_its_stream
 def md_coselect_pair_stats(idx_prev, idx_l, idx_next, E, T_fit=None, C2=None, accumulate=False,
                            dev_status=None, stream=None):
     """Pair counts C2[a, b, e'] (int32 view of uint32 [E, E, E])."""
@@ -561,6 +592,7 @@ def md_coselect_pair_stats(idx_prev, idx_l, idx_next, E, T_fit=None, C2=None, ac
     return C2
 
 
+@_on_its_stream
 def md_token_shuffle_pair(idx_prev, idx_l, C, C2, expert_to_rank_next, R, min_obs, pred_rank=None,
                           perm=None, inv=None, use_pair=None, workspace=None, dev_status=None,
                           stream=None):
@@ -636,15 +668,12 @@ def _tail(dev_status, stream, dev):
     return dev_status, torch.cuda.current_stream(dev).cuda_stream
 
 
-# the current stream's handle without the Stream object around it (2 us a call)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def md_set_expert_path(path=MD_EXPERT_AUTO):
     """Choose the kernel form of the expert products (tests and tuning)."""
     _check(_call("md_set_expert_path", "cpu", int(path)), "md_set_expert_path")
 
 
+@_on_its_stream
 def md_expert_gemm(x, w, expert_offsets, expert_counts, w_layout=MD_W_NK, out=None,
                    dev_status=None, stream=None):
     """y[r] = x[r] times the matrix of row r's expert (MD_W_NK: w [E, N, K], MD_W_KN: w [E, K, N]).
@@ -672,6 +701,7 @@ def md_expert_gemm(x, w, expert_offsets, expert_counts, w_layout=MD_W_NK, out=No
     return out
 
 
+@_on_its_stream
 def md_expert_gated(x, w, expert_offsets, expert_counts, keep=False, out=None, codes=None,
                     scales=None, dev_status=None, stream=None):
     """Gated up-projection act = silu(g) * u with g, u = x w[e]^T; w [E, 2F, K] holds g's rows, then u's.
@@ -710,6 +740,7 @@ def md_expert_gated(x, w, expert_offsets, expert_counts, keep=False, out=None, c
     return (out, codes, scales) if keep else out
 
 
+@_on_its_stream
 def md_expert_wgrad(dy, x, expert_offsets, expert_counts, out_dtype=torch.float32, dw=None,
                     accumulate=False, dev_status=None, stream=None):
     """dw[e] = sum over expert e's rows of dy[r]^T x[r], [E, N, K]; accumulate adds into a float32 dw.
@@ -743,6 +774,7 @@ def md_expert_wgrad(dy, x, expert_offsets, expert_counts, out_dtype=torch.float3
     return dw
 
 
+@_on_its_stream
 def md_expert_gated_backward(da, codes, scales, dh=None, act=None, want_act=True, stream=None):
     """(dh, act) from the gradient of the activation and the checkpoint of md_expert_gated.
 
@@ -767,6 +799,7 @@ def md_expert_gated_backward(da, codes, scales, dh=None, act=None, want_act=True
     return dh, act
 
 
+@_on_its_stream
 def md_combine_backward(dout, assign_row, topk_w, y=None, y_rows=None, dy=None, dw=None,
                         dev_status=None, stream=None):
     """Gradient of md_combine: (dy, dw), dy[assign_row[t, j]] = topk_w[t, j] dout[t].
@@ -857,6 +890,7 @@ def md_exchange_plan(src_rank_offsets, me):
     return list(base), list(recv)
 
 
+@_on_its_stream
 def md_dispatch_exchange(x, topk_idx, topk_w, expert_to_rank, E, row_of_slot, rank_offsets,
                          token_base, peers, dev_status=None, stream=None):
     """Write this rank's dispatch rows (and their metadata) into the R
@@ -881,6 +915,7 @@ def md_dispatch_exchange(x, topk_idx, topk_w, expert_to_rank, E, row_of_slot, ra
     _check(rc, "md_dispatch_exchange")
 
 
+@_on_its_stream
 def md_combine_partials(y, y_row, slot_idx, slot_w, out=None, dev_status=None, stream=None):
     """Return rows of a receiving rank: z[i] = bf16(sum over carried slots, by
     ascending expert, of slot_w * y[y_row])."""
@@ -903,6 +938,7 @@ def md_combine_partials(y, y_row, slot_idx, slot_w, out=None, dev_status=None, s
     return out
 
 
+@_on_its_stream
 def md_combine_exchange(peers, topk_idx, expert_to_rank, E, row_of_slot, rank_offsets, H,
                         out=None, dev_status=None, stream=None):
     """out[t] = bf16(fp32 sum, by ascending rank, of the return rows of t read
@@ -929,6 +965,7 @@ def md_combine_exchange(peers, topk_idx, expert_to_rank, E, row_of_slot, rank_of
 
 # ------------------------------------------------------------ statistics
 
+@_on_its_stream
 def md_rank_stats(topk_idx, E, R, expert_to_rank, hist=None, dev_status=None, stream=None):
     """hist int64 [k+1]: tokens whose experts sit on exactly D distinct ranks."""
     _need(topk_idx, "topk_idx", torch.int32)
@@ -955,6 +992,7 @@ def table1_row(hist):
     return out[0], out[1], out[2]
 
 
+@_on_its_stream
 def md_successor_share(C, W, stream=None):
     """(num, den) int32 views of uint32 [E]: max_e' C[e, e'] and W[e, e]."""
     _need(C, "C", torch.int32)
@@ -970,6 +1008,7 @@ def md_successor_share(C, W, stream=None):
     return num, den
 
 
+@_on_its_stream
 def md_count_sums(x, y, stream=None):
     """Exact (sx, sy, sxx, syy, sxy) of two count tables (int32 views of uint32)."""
     _need(x, "x", torch.int32)
