@@ -3,8 +3,9 @@
 Argument marshalling only: every function checks tensor placement, dtype and
 contiguity, allocates outputs with torch when the caller passes none, and calls
 the C entry point of the same name on the current CUDA stream, or as in
-`torch.cuda.stream(stream)` where `stream=` is given.  All arithmetic runs in the library's kernels.  If libmoedispatch.so is missing the first call
-raises; there is no fallback.
+`torch.cuda.stream(stream)` where `stream=` is given.  All arithmetic runs in
+the library's kernels.  If libmoedispatch.so is missing the first call raises;
+there is no fallback.
 """
 from __future__ import annotations
 

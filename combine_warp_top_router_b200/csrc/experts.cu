@@ -1141,10 +1141,6 @@ bool too_large(int64_t rows, int E, int64_t N, int64_t K)
 
 constexpr int64_t kMostTiles = (int64_t)1 << 30;
 
-// Row tiles of `most` rows that E ranges of `rows` rows make, at most: sum of ceil(c / most)
-// <= rows / most + (experts with rows) (1 - 1 / most).
-int64_t most_row_tiles(int64_t rows, int E, int most) { return rows / most + (rows < E ? rows : E); }
-
 template <int MODE>
 int run_few(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int64_t d1, cudaStream_t s)
 {
@@ -1155,7 +1151,7 @@ int run_few(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int
         return MD_ERR_CUDA;
     const int mt = (a.n + P::kWidth - 1) / P::kWidth;
     a.mt = FastDiv((uint32_t)mt);
-    a.row_tiles = most_row_tiles(rows, a.E, P::BN);
+    a.row_tiles = md::ragged_most_tiles(rows, a.E, P::BN);
     const int64_t tiles = a.row_tiles * mt;
     if (tiles > kMostTiles) return MD_ERR_UNSUPPORTED;
     // Few tiles leave SMs idle and each tile streams its weights through one SM: clusters of
@@ -1188,7 +1184,7 @@ int run_wide(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, in
     if (!md::make_map(&ma, w, kBf16, 2, d0, d1, a.E, 64, MODE == kNK ? kTileM : 64) ||
         !md::make_map(&mb, x, kBf16, 2, a.k, rows, 0, 64, 64))
         return MD_ERR_CUDA;
-    a.row_tiles = most_row_tiles(rows, a.E, 256);
+    a.row_tiles = md::ragged_most_tiles(rows, a.E, 256);
     a.subs = subs_for(a.row_tiles * ((a.n + W::kSub - 1) / W::kSub), 4);
     const int mt = (a.n + a.subs * W::kSub - 1) / (a.subs * W::kSub);
     a.mt = FastDiv((uint32_t)mt);
@@ -1198,18 +1194,12 @@ int run_wide(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, in
                   mb, mb, a);
 }
 
-// Which form.  With 64 rows to an expert and fewer a call is bound by reading the
-// weights, and k_expert_few's deeper ring of weights does that better; above, its narrow tiles
-// read them again for every 64 rows (64 experts of 2048 x 2048, us, few / wide: 16 rows 84 / 91,
-// 64 rows 91 / 98, 96 rows 108 / 101, 256 rows 227 / 128).  A call with no more wide tiles
-// than there are SM pairs takes the narrow ones at any length (8 experts of 256
-// rows, 1024 x 1024: 11 / 13; of 512 rows 18 / 13).  `sub`: output columns of a wide tile.
+// Which form: few, or wide (ragged_few has the rule).
 bool few_rows(int64_t rows, int E, int64_t columns, int sub)
 {
     const int path = md::expert_path();
     if (path != MD_EXPERT_AUTO) return path == MD_EXPERT_FEW;
-    const int64_t wide = most_row_tiles(rows, E, 256) * ((columns + sub - 1) / sub);
-    return rows <= (int64_t)64 * E || wide <= md::sm_count() / 2;
+    return md::ragged_few(rows, E, columns, sub, md::sm_count());
 }
 
 }  // namespace
