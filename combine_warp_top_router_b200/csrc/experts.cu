@@ -82,8 +82,8 @@ struct Shared {
     uint32_t tmem;
     int abort;
     unsigned loads;  // counts up as the loading warp goes on: a sign of life for the other roles' waits
-    int tiles;  // ragged row tiles of all experts
-    int64_t sums[12];
+    int tiles;  // ragged row tiles of all experts; -1: more than there can be
+    int sums[12];
 };
 
 // Bounded wait of a converged warp; all lanes get the same answer.  The first look
@@ -230,7 +230,8 @@ __device__ __forceinline__ void sort_experts(const Table &tab, const Args &a)
 
 // Exclusive running sum of the experts' row tiles, by all threads; barriers inside.  Ranges that
 // overlap so far that they make more tiles than the rows can (and more than the host
-// has allowed for) are reported, and no tile is left.
+// has allowed for) leave -1: no tiles, and a report at the kernel's end (here it
+// would cost a one-token call 0.1 us).
 template <int BN>
 __device__ __forceinline__ void count_tiles(const Table &tab, Shared *sh, const Args &a)
 {
@@ -239,10 +240,10 @@ __device__ __forceinline__ void count_tiles(const Table &tab, Shared *sh, const 
     for (int e0 = 0; e0 < a.E; e0 += blockDim.x) {
         const int e = e0 + threadIdx.x;
         const int own = e < a.E ? md::ragged_tiles(tab.cnt(tab.order(e)), BN) : 0;
-        int64_t v = own;
+        int v = own;  // an expert has 2^25 tiles at most, 32 of them 2^30
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
+            const int o = __shfl_up_sync(0xffffffffu, v, d);
             if (lane >= d) v += o;
         }
         if (lane == 31) sh->sums[warp] = v;
@@ -255,13 +256,7 @@ __device__ __forceinline__ void count_tiles(const Table &tab, Shared *sh, const 
         if (e < a.E) tab.pre(e) = (int)(before + v - own);
         __syncthreads();
     }
-    if (threadIdx.x == 0) {
-        if (run > a.row_tiles) {
-            md::report(a.status, MD_ERR_DATA);
-            run = 0;
-        }
-        sh->tiles = (int)run;
-    }
+    if (threadIdx.x == 0) sh->tiles = run > a.row_tiles ? -1 : (int)run;
 }
 
 // Rows of row tile rt; a converged warp, which looks at 32 places of the order at once.
@@ -474,7 +469,7 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
     const uint32_t tmem = sh->tmem;
 
     const int first = blockIdx.x / a.split, step = gridDim.x / a.split;
-    const int total = sh->tiles * (int)a.mt.d;  // the host keeps it below 2^30
+    const int total = max(sh->tiles, 0) * (int)a.mt.d;  // the host keeps it below 2^30
     const uint32_t sbase = md::smem_addr(base);
     // blocks of the contraction: [kb0, kb1) in this CTA
     const int kblocks = (a.k + kTileK - 1) / kTileK;
@@ -605,6 +600,7 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
         }
     }
 
+    if (threadIdx.x == 0 && sh->tiles < 0) md::report(a.status, MD_ERR_DATA);
     // ---- end: nobody leaves while its cluster may still read its shared memory
     __syncwarp();
     md::tmem_fence_before();
@@ -764,7 +760,7 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
 
     const int width = a.subs * W::kSub;  // output columns (weight gradient: rows of dw) of a tile
     const int mt = (int)a.mt.d;
-    const int total = kWg ? a.E * (int)a.per.d : sh->tiles * mt;  // the host keeps it below 2^30
+    const int total = kWg ? a.E * (int)a.per.d : max(sh->tiles, 0) * mt;  // the host keeps it below 2^30
     const int step = gridDim.x / 2, place = blockIdx.x / 2, rounds = (total + step - 1) / step;
     // the cluster's tile of a round, dealt back and forth; `total` or more: none
     auto deal = [&](int round) { return round * step + (round & 1 ? step - 1 - place : place); };
@@ -1073,6 +1069,7 @@ __global__ void __launch_bounds__(Wide<MODE>::kThreads, 1)
     }
 
     if (kWg) md::bulk_wait_all();
+    if (!kWg && threadIdx.x == 0 && sh->tiles < 0) md::report(a.status, MD_ERR_DATA);
     // ---- end: nobody leaves while its pair may still read its shared memory
     __syncwarp();
     md::tmem_fence_before();
