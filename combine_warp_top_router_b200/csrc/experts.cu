@@ -484,8 +484,8 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
     if (warp == kLoadWarp) {
         // ------------------------------------------------ loads
         Turn at(P::kStages);
-        int used = 0;         // stages loaded at least once
-            unsigned begun = 0;  // signs of life
+        int used = 0;        // stages loaded at least once
+        unsigned begun = 0;  // signs of life
         bool ok = true;
         for (int t = first; ok && t < total; t += step) {
             const Tile q = tile_of(t);
@@ -637,9 +637,11 @@ __global__ void __launch_bounds__(Few<MODE>::kThreads, 1)
 // each CTA.  For such a block the second CTA awaits its loads on a barrier of
 // its own, clears, and tells the first; passing every stage on this way took a
 // quarter of the loads' rate.  The tensor cores drop low bits at each
-// addition: summed whole, 131072 rows over 128 experts are off by 1.6e-6 (2-norm).  float32
-// results are therefore summed in TMEM over kSegment blocks at most, in equal shares, and
-// then added in dw, in order: 0.9e-6, for 5% of the time.  (32 blocks: 1.1e-6.)
+// addition, and a sum of n rows summed whole is off by some 1.2e-9 n (2-norm, normal data):
+// 5.3e-5 for an expert of 46080 rows.  float32 results are therefore summed in TMEM over
+// kSegment blocks at most, in equal shares, and then added in dw, in order: 1.1e-6 there.
+// Of 131072 skewed rows over 128 experts 1.6e-6 becomes 0.9e-6, for 5% of the time (32
+// blocks: 1.1e-6).
 constexpr int kSegment = 18;
 
 constexpr int kLaunchRegisters = 168;  // 12 warps of them: the sum of the split 8 x 216 + 4 x 72
@@ -1163,9 +1165,9 @@ int run_few(const void *x, const void *w, int64_t rows, Args &a, int64_t d0, int
 }
 
 // Two subs to a tile where that still gives the pairs of SMs several tiles each: from four
-// tiles of one sub to a pair (16 experts of 384 rows, 2048 x 2048, one sub / two: 53 / 47 us; of
-// 256 rows 36 / 37; 8 experts of 512 rows, 2048 x 1024: 19 / 28), for the weight gradient
-// from eight (8 experts of 256 rows, 2048 x 2048: 32 / 37; 16 of 512 rows 86 / 79).
+// tiles of one sub to a pair (16 experts of 384 rows, 2048 x 2048, one sub / two: 53 / 48 us; of
+// 256 rows 37 / 37; 8 experts of 512 rows, 2048 x 1024: 19 / 28), for the weight gradient
+// from eight (8 experts of 256 rows, 2048 x 2048: 32 / 38; 16 of 512 rows 88 / 82).
 inline int subs_for(int64_t tiles_of_one, int to_a_pair)
 {
     const int path = md::expert_path();

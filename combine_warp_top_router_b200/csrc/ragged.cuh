@@ -29,8 +29,8 @@ MD_BOTH int64_t ragged_most_tiles(int64_t rows, int E, int most) { return rows /
 
 // Whether a call takes k_expert_few.  With 64 rows to an expert and fewer it is bound by reading the
 // weights, and that kernel's deeper ring of weights does that better; above, its narrow tiles
-// read them again for every 64 rows (64 experts of 2048 x 2048, us, few / wide: 16 rows 84 / 91,
-// 64 rows 91 / 98, 96 rows 108 / 101, 256 rows 227 / 128).  A call with no more wide tiles
+// read them again for every 64 rows (64 experts of 2048 x 2048, us, few / wide: 16 rows 83 / 90,
+// 64 rows 98 / 94, 96 rows 159 / 96, 256 rows 377 / 119).  A call with no more wide tiles
 // than there are SM pairs leaves SMs idle in the wide form, and takes the narrow tiles as long as
 // those make one and a half rounds of the SMs at most.  1 to 32 experts, K and N of 256 to 4096, few / wide:
 // 0.5 to 1.3 in one round and 0.6 to 1.3 in one and a half, below 1 but for K = 4096, 0.7 to 2.1 in
