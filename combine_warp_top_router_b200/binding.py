@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 import threading
 from dataclasses import dataclass
@@ -167,9 +168,15 @@ def _on_its_stream(fn):
     """With `stream=` given the call runs as in `torch.cuda.stream(stream)`: what it allocates, outputs
     and scratch, then belongs to that stream.  Memory of the current stream may be freed there while
     kernels still use it, and the call on the other stream would write into it."""
+    last = list(inspect.signature(fn).parameters).index("stream")
+
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        if stream is None or (_raw_stream is not None and _raw_stream(stream.device_index) == stream.cuda_stream):
+        if stream is None and len(args) == last + 1:  # given by position
+            args, stream = args[:last], args[last]
+        if stream is None:
+            return fn(*args, **kw)
+        if _raw_stream is not None and _raw_stream(stream.device_index) == stream.cuda_stream:
             return fn(*args, stream=stream, **kw)  # already the current one
         with torch.cuda.stream(stream):
             return fn(*args, stream=stream, **kw)

@@ -203,6 +203,8 @@ def test_as_many_rows_as_there_may_be():
     the middle."""
     rows = 2 ** 31 - 4097
     torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 69 GB")
     x = torch.zeros(rows, 8, dtype=torch.bfloat16, device=DEV)
     parts = [slice(0, 700), slice(2 ** 30 - 300, 2 ** 30 + 300), slice(rows - 700, rows)]
     for i, p in enumerate(parts):
